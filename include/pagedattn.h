@@ -137,6 +137,62 @@ pa_status_t pa_kv_append(const pa_kv_pool_t *pool, const void *k_new,
                          int32_t max_pages, int32_t *d_err, void *stream);
 
 /*
+ * Rotary position embedding (the pages do not fix one; every served model of
+ * the shapes they discuss rotates its queries and keys before Eq. 1). Pair j,
+ * 0 <= j < rotary_dim / 2, of a head's row x is (a, b) = (x[j], x[j +
+ * rotary_dim / 2]), or (x[2j], x[2j + 1]) when interleaved != 0, and becomes
+ *   a' = a c - b s,   b' = b c + a s,   c = table[p][j], s = table[p][rotary_dim / 2 + j]
+ * with p the token's position on axis axis_of_pair[j]. The products and sums
+ * are fp32, each rounded once (no fused multiply-add), and a', b' are rounded
+ * to bf16 (nearest even). Elements at and past rotary_dim pass unchanged.
+ * Text models use one axis; models that place image and video tokens in time,
+ * height and width give every pair one of three.
+ */
+typedef struct {
+  const float *table;     /* (device) fp32 [table_len][rotary_dim], 16-byte aligned: row p
+                             holds the cosines, then the sines, of position p */
+  int32_t table_len;      /* positions 0 .. table_len - 1                         */
+  int32_t rotary_dim;     /* a multiple of 16, at most head_dim                   */
+  int32_t interleaved;    /* 0: pairs half of rotary_dim apart; else neighbours   */
+  int32_t num_axes;       /* position axes, 1..4                                  */
+  uint8_t axis_of_pair[64]; /* axis of pair j, below num_axes (j < rotary_dim / 2) */
+} pa_rope_t;
+
+/*
+ * pa_kv_append_rope — pa_kv_append with the rotation of pa_rope_t applied to
+ * the new tokens' queries and keys on the way: one launch that writes q_out
+ * and the page slots. The stored bits are those of rotating k_new (rounded to
+ * bf16) and calling pa_kv_append on the result; values are not rotated.
+ *
+ *   q         : (device) bf16, token i's row [num_q_heads][head_dim] at
+ *               q + i * q_stride; NULL when num_q_heads == 0 (keys only)
+ *   q_out     : (device) bf16 [num_tokens][num_q_heads][head_dim], dense; may
+ *               be q itself (then q_stride must be num_q_heads * head_dim), and
+ *               must not overlap any input otherwise
+ *   k_new, v_new : (device) bf16, token i's row [num_kv_heads][head_dim] at
+ *               k_new + i * k_stride, v_new + i * v_stride
+ *   q_stride, k_stride, v_stride : elements between tokens, multiples of 8 and
+ *               at least one row, so the three parts of a fused projection's
+ *               output are read in place
+ *   rope_pos  : (device) int32 [num_axes][num_tokens], token i's position on
+ *               each axis; NULL: pos on every axis
+ * Other arguments as for pa_kv_append. A token whose sequence, position or
+ * page is out of range is flagged and not stored, but its query is rotated; a
+ * rotation position outside [0, table_len) flags PA_DERR_BAD_POS and nothing
+ * of that token is written. num_tokens == 0 is a no-op.
+ * The kernel is launched as a programmatic dependent of the previous kernel on
+ * the stream and waits for it before reading any input.
+ */
+pa_status_t pa_kv_append_rope(const pa_kv_pool_t *pool, const pa_rope_t *rope,
+                              const void *q, int64_t q_stride, int32_t num_q_heads,
+                              void *q_out, const void *k_new, int64_t k_stride,
+                              const void *v_new, int64_t v_stride,
+                              const int32_t *seq_idx, const int32_t *pos,
+                              const int32_t *rope_pos, int32_t num_tokens,
+                              const int32_t *block_tables, int32_t num_seqs,
+                              int32_t max_pages, int32_t *d_err, void *stream);
+
+/*
  * pa_decode_append_lens — pa_decode_append with the context lengths also given
  * in host memory (host_context_lens: int32 [num_seqs], the values in
  * context_lens as the host knows them, e.g. from a serving scheduler; may be

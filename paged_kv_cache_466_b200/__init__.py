@@ -9,6 +9,8 @@ Entry points (same names as the C ABI, see include/pagedattn.h):
 
 * ``pa_kv_append``       — write new tokens' K/V into their page slots
                            (quantising for an INT8 pool, Eq. 3)
+* ``pa_kv_append_rope``  — the same cache write with rotary positions applied to
+                           the new queries and keys on the way
 * ``pa_decode``          — Eq. 1 decode attention over the paged cache
 * ``pa_splitkv_reduce``  — log-sum-exp merge of split-KV partials
 * ``pa_validate_tables`` — device-side page-table check
@@ -22,7 +24,8 @@ Entry points (same names as the C ABI, see include/pagedattn.h):
                            that cannot allocate device memory (the scratch is
                            a fixed-size array owned by the library)
 
-``KVPool`` owns the page pool tensors; ``pages`` holds the host-side page
+``KVPool`` owns the page pool tensors; ``Rope`` describes a rotary position
+embedding; ``pages`` holds the host-side page
 allocator and cache-size formulas.
 """
 from __future__ import annotations
@@ -38,9 +41,9 @@ from ._lib import (PA_DERR_BAD_CTX, PA_DERR_BAD_PAGE, PA_DERR_BAD_POS, PA_DERR_B
                    PA_STEP_NEWEST_PER_SEQ,
                    PA_DERR_TIMEOUT,
                    PA_KV_BF16, PA_KV_FP8_PER_TOKEN, PA_KV_U4_PER_TOKEN, PA_KV_U8_PER_TOKEN,
-                   PagedAttnError, pa_kv_pool_t)
+                   PagedAttnError, pa_kv_pool_t, pa_rope_t)
 
-__all__ = ["KVPool", "pa_kv_append", "pa_decode", "pa_decode_append", "pa_decode_noalloc", "pa_splitkv_reduce",
+__all__ = ["KVPool", "Rope", "pa_kv_append", "pa_kv_append_rope", "pa_decode", "pa_decode_append", "pa_decode_noalloc", "pa_splitkv_reduce",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_bytes",
            "pa_decode_window", "pa_decode_window_workspace_bytes",
            "pa_decode_range", "pa_decode_range_workspace_bytes", "pa_merge_partials",
@@ -87,6 +90,14 @@ def _need(t: torch.Tensor, name: str, dtype, device=None):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _need_device(device, where: str, d_err: Optional[torch.Tensor]):
+    """The call runs on the current device: the pool must be there, and the error word."""
+    if device.type != "cuda" or device.index not in (None, torch.cuda.current_device()):
+        raise ValueError(f"{where}: the pool is on {device}, not on the current CUDA device")
+    if d_err is not None:
+        _need(d_err, "d_err", torch.int32, device)
+
+
 class KVPool:
     """The physical page pool: K and V as [num_pages, Hkv, P, D] tensors:
     ``dtype`` "bf16", "u8" (INT8 codes, Eq. 3), "fp8" (E4M3 codes) or "u4"
@@ -127,6 +138,37 @@ class KVPool:
     @property
     def device(self):
         return self.k.device
+
+
+class Rope:
+    """A rotary position embedding: ``table`` fp32 [positions, rotary_dim], row p
+    the cosines then the sines of position p; pairs half of rotary_dim apart,
+    or neighbouring elements when ``interleaved``. ``axis_of_pair`` (one entry
+    per pair) gives every pair the position axis it follows (time, height,
+    width); by default all pairs follow one axis."""
+
+    def __init__(self, table: torch.Tensor, interleaved: bool = False, axis_of_pair=None):
+        _need(table, "table", torch.float32)
+        if table.dim() != 2 or table.shape[1] % 2 != 0 or table.shape[1] > 128:
+            raise ValueError("Rope: table must be [positions, rotary_dim], rotary_dim <= 128")
+        half = table.shape[1] // 2
+        axes = [0] * half if axis_of_pair is None else [int(a) for a in axis_of_pair]
+        if len(axes) != half or min(axes) < 0 or max(axes) > 3:
+            raise ValueError(f"Rope: axis_of_pair must hold {half} axes in 0..3")
+        self.table, self.interleaved, self.num_axes = table, bool(interleaved), max(axes) + 1
+        self._c = pa_rope_t(table.data_ptr(), table.shape[0], table.shape[1], int(interleaved),
+                            self.num_axes, (ctypes.c_uint8 * 64)(*axes))
+
+    @classmethod
+    def from_base(cls, positions: int, rotary_dim: int, base: float = 10000.0, device="cuda", **kw):
+        """The table of angles p * base^(-2j / rotary_dim), computed in 64 bits."""
+        inv = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+        ang = torch.arange(positions, dtype=torch.float64)[:, None] * inv
+        return cls(torch.cat([ang.cos(), ang.sin()], 1).float().to(device), **kw)
+
+    @property
+    def c(self) -> pa_rope_t:
+        return self._c
 
 
 def pa_derr_status(derr: int) -> int:
@@ -189,6 +231,63 @@ def pa_kv_append(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, seq_idx
                                   _ptr(pos), n, _ptr(block_tables), block_tables.shape[0],
                                   block_tables.shape[1], _ptr(d_err), _stream(stream))
     _lib.check(st, "pa_kv_append")
+
+
+def _token_rows(t: torch.Tensor, name: str, heads: int, dim: int, device) -> int:
+    """Elements between the tokens of bf16 [N, heads, dim], each token's rows dense."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def pa_kv_append_rope(pool: KVPool, rope: Rope, q: Optional[torch.Tensor], k_new: torch.Tensor,
+                      v_new: torch.Tensor, seq_idx: torch.Tensor, pos: torch.Tensor,
+                      block_tables: torch.Tensor, rope_pos: Optional[torch.Tensor] = None,
+                      q_out: Optional[torch.Tensor] = None,
+                      d_err: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotate the new tokens' queries q [N, Hq, D] (returned, or written to
+    ``q_out``, which may be q) and keys k_new [N, Hkv, D] by their positions
+    and write keys and values into their page slots, in one launch. The token
+    stride of q, k_new and v_new is free (the slices of a fused projection's
+    output). ``rope_pos`` int32 [num_axes, N] are the positions on each axis
+    (default: ``pos`` on all). q may be None: keys and values only."""
+    dev = pool.device
+    _need_device(dev, "pa_kv_append_rope", d_err)
+    n, D = seq_idx.numel(), pool.head_dim
+    ks = _token_rows(k_new, "k_new", pool.num_kv_heads, D, dev)
+    vs = _token_rows(v_new, "v_new", pool.num_kv_heads, D, dev)
+    _need(seq_idx, "seq_idx", torch.int32, dev)
+    _need(pos, "pos", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    if rope.table.device != dev:
+        raise ValueError(f"the rotation's table must be on {dev}, got {rope.table.device}")
+    hq = qs = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _token_rows(q, "q", hq, D, dev)
+        if q_out is None:
+            q_out = torch.empty((q.shape[0], hq, D), dtype=torch.bfloat16, device=dev)
+        _need(q_out, "q_out", torch.bfloat16, dev)
+        if q.shape[0] != n or q_out.shape != q.shape:
+            raise ValueError("pa_kv_append_rope: shape mismatch")
+    if rope_pos is not None:
+        _need(rope_pos, "rope_pos", torch.int32, dev)
+        if rope_pos.numel() != rope.num_axes * n:
+            raise ValueError("pa_kv_append_rope: rope_pos must be [num_axes, tokens]")
+    if k_new.shape[0] != n or v_new.shape[0] != n or pos.numel() != n or block_tables.dim() != 2:
+        raise ValueError("pa_kv_append_rope: shape mismatch")
+    st = _lib.load().pa_kv_append_rope(
+        ctypes.byref(pool.c), ctypes.byref(rope.c), _ptr(q), qs, hq, _ptr(q_out), _ptr(k_new), ks,
+        _ptr(v_new), vs, _ptr(seq_idx), _ptr(pos), _ptr(rope_pos), n, _ptr(block_tables),
+        block_tables.shape[0], block_tables.shape[1], _ptr(d_err), _stream(stream))
+    _lib.check(st, "pa_kv_append_rope")
+    return q_out
 
 
 def pa_decode(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,

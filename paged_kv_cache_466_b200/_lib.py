@@ -48,12 +48,27 @@ class pa_kv_pool_t(ctypes.Structure):
     ]
 
 
+class pa_rope_t(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("table_len", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("num_axes", ctypes.c_int32),
+        ("axis_of_pair", ctypes.c_uint8 * 64),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _POOL = ctypes.POINTER(pa_kv_pool_t)
+_ROPE = ctypes.POINTER(pa_rope_t)
+_L = ctypes.c_int64
 
 SIGNATURES = {
     "pa_kv_append": (_I, [_POOL, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P]),
+    "pa_kv_append_rope": (_I, [_POOL, _ROPE, _P, _L, _I, _P, _P, _L, _P, _L, _P, _P, _P, _I, _P, _I,
+                               _I, _P, _P]),
     "pa_derr_status": (_I, [_I]),
     "pa_selftest_wait_timeout": (_I, [_I, _P, _P]),
     "pa_decode_auto_splits": (_I, [_I, _I, _I, _I]),

@@ -181,6 +181,95 @@ pa_status_t pa_kv_append(const pa_kv_pool_t *pool, const void *k_new, const void
                      "pa_kv_append launch");
 }
 
+namespace {
+
+pa_status_t check_rope(const pa_rope_t *rope, int head_dim) {
+  if (rope == nullptr) return fail(PA_ERR_INVALID_ARG, "rope is NULL");
+  if (rope->table == nullptr || rope->table_len <= 0)
+    return fail(PA_ERR_INVALID_ARG, "rope: table is NULL or table_len=%d", rope->table_len);
+  if (!aligned(rope->table, 16))
+    return fail(PA_ERR_INVALID_ARG, "rope: table must be 16-byte aligned");
+  if (rope->rotary_dim <= 0 || rope->rotary_dim % 16 != 0 || rope->rotary_dim > head_dim)
+    return fail(PA_ERR_UNSUPPORTED, "rope: rotary_dim=%d (a multiple of 16, at most %d)",
+                rope->rotary_dim, head_dim);
+  if (rope->num_axes < 1 || rope->num_axes > 4)
+    return fail(PA_ERR_UNSUPPORTED, "rope: num_axes=%d (1..4)", rope->num_axes);
+  for (int j = 0; j < rope->rotary_dim / 2; ++j)
+    if (rope->axis_of_pair[j] >= rope->num_axes)
+      return fail(PA_ERR_INVALID_ARG, "rope: axis_of_pair[%d]=%d with %d axes", j,
+                  rope->axis_of_pair[j], rope->num_axes);
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status_t pa_kv_append_rope(const pa_kv_pool_t *pool, const pa_rope_t *rope, const void *q,
+                              int64_t q_stride, int32_t num_q_heads, void *q_out,
+                              const void *k_new, int64_t k_stride, const void *v_new,
+                              int64_t v_stride, const int32_t *seq_idx, const int32_t *pos,
+                              const int32_t *rope_pos, int32_t num_tokens,
+                              const int32_t *block_tables, int32_t num_seqs, int32_t max_pages,
+                              int32_t *d_err, void *stream) {
+  g_last_error.clear();
+  pa_status_t st = check_pool(pool);
+  if (st == PA_OK) st = check_rope(rope, pool->head_dim);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || num_seqs < 0 || max_pages <= 0 || num_q_heads < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_tokens=%d num_seqs=%d max_pages=%d num_q_heads=%d",
+                num_tokens, num_seqs, max_pages, num_q_heads);
+  if (num_q_heads > 65535 || pool->num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "num_q_heads and num_kv_heads must be <= 65535");
+  if (num_tokens == 0) return PA_OK;
+  if (!k_new || !v_new || !seq_idx || !pos || !block_tables)
+    return fail(PA_ERR_INVALID_ARG, "k_new, v_new, seq_idx, pos and block_tables are required");
+  if (num_q_heads > 0 && (!q || !q_out))
+    return fail(PA_ERR_INVALID_ARG, "q and q_out are required with num_q_heads > 0");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q, 16) || !aligned(q_out, 16))
+    return fail(PA_ERR_INVALID_ARG, "q, q_out, k_new and v_new must be 16-byte aligned");
+  const int64_t q_row = (int64_t)num_q_heads * pool->head_dim;
+  const int64_t kv_row = (int64_t)pool->num_kv_heads * pool->head_dim;
+  if ((num_q_heads > 0 && (q_stride < q_row || q_stride % 8 != 0)) || k_stride < kv_row ||
+      k_stride % 8 != 0 || v_stride < kv_row || v_stride % 8 != 0)
+    return fail(PA_ERR_INVALID_ARG,
+                "q_stride=%lld k_stride=%lld v_stride=%lld (multiples of 8, at least one row)",
+                (long long)q_stride, (long long)k_stride, (long long)v_stride);
+  if (num_q_heads > 0 && q == q_out && q_stride != q_row)
+    return fail(PA_ERR_INVALID_ARG, "rotating q in place needs dense rows");
+  AppendRopeArgs a;
+  a.q = static_cast<const unsigned char *>(q);
+  a.k_new = static_cast<const unsigned char *>(k_new);
+  a.v_new = static_cast<const unsigned char *>(v_new);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<unsigned char *>(q_out);
+  a.hq = num_q_heads;
+  a.n = num_tokens;
+  a.seq_idx = seq_idx;
+  a.pos = pos;
+  a.block_tables = block_tables;
+  a.num_seqs = num_seqs;
+  a.max_pages = max_pages;
+  a.num_pages = pool->num_pages;
+  a.hkv = pool->num_kv_heads;
+  a.P = pool->page_size;
+  a.k_pool = static_cast<unsigned char *>(pool->k_pool);
+  a.v_pool = static_cast<unsigned char *>(pool->v_pool);
+  a.k_sz = pool->k_sz;
+  a.v_sz = pool->v_sz;
+  a.d_err = d_err;
+  a.table = rope->table;
+  a.table_len = rope->table_len;
+  a.rot = rope->rotary_dim;
+  a.num_axes = rope->num_axes;
+  a.rope_pos_axes = rope_pos != nullptr ? rope->num_axes : 1;
+  a.rope_pos = rope_pos != nullptr ? rope_pos : pos;
+  std::memcpy(a.axis_of_pair, rope->axis_of_pair, sizeof a.axis_of_pair);
+  return cuda_status(launch_append_rope(pool->head_dim, pool->dtype, a, rope->interleaved != 0,
+                                        static_cast<cudaStream_t>(stream)),
+                     "pa_kv_append_rope launch");
+}
+
 int32_t pa_prefix_plan_splits(int64_t units, int32_t tiles, int32_t num_sms,
                               int32_t decode_ctas_per_sm, double suffix_bytes) {
   if (units <= 0 || tiles <= 0 || num_sms <= 0 || decode_ctas_per_sm <= 0 ||

@@ -123,6 +123,40 @@ cudaError_t launch_kv_append(const pa_kv_pool_t &pool, const void *k_new,
                              int32_t max_pages, int32_t *d_err,
                              cudaStream_t stream);
 
+// pa_kv_append_rope: rows of q, k and v (strides in elements between tokens).
+struct AppendRopeArgs {
+  const unsigned char *q;
+  const unsigned char *k_new;
+  const unsigned char *v_new;
+  int64_t q_stride, k_stride, v_stride;
+  unsigned char *q_out;  // bf16 [n][hq][D]; may be q
+  int32_t hq;            // 0: no queries
+  int32_t n;
+  const int32_t *seq_idx;
+  const int32_t *pos;
+  const int32_t *block_tables;
+  int32_t num_seqs;
+  int32_t max_pages;
+  int32_t num_pages;
+  int32_t hkv;
+  int32_t P;
+  unsigned char *k_pool;
+  unsigned char *v_pool;
+  float *k_sz;
+  float *v_sz;
+  int32_t *d_err;
+  const float *table;  // [table_len][rot]
+  int32_t table_len;
+  int32_t rot;
+  int32_t num_axes;
+  int32_t rope_pos_axes;    // rows of rope_pos: num_axes, or 1 for all axes
+  const int32_t *rope_pos;  // [rope_pos_axes][n]
+  uint8_t axis_of_pair[64];
+};
+
+cudaError_t launch_append_rope(int D, int kv_dtype, const AppendRopeArgs &a, bool interleaved,
+                               cudaStream_t stream);
+
 cudaError_t launch_validate_tables(const int32_t *block_tables, int32_t B,
                                    int32_t max_pages, const int32_t *ctx,
                                    int32_t num_pages, int32_t page_size,

@@ -126,5 +126,57 @@ __device__ __forceinline__ void quantise_row_u4(const unsigned char *src_row,
   if (lane == 0) *reinterpret_cast<float2 *>(dst_sz) = make_float2(s, z);
 }
 
+// The same quantisers for a row held by kLanes neighbouring lanes (kLanes a
+// power of two, lane groups aligned) with 16 bf16-valued elements each:
+// x[0..7] and x[8..15] are two 8-element chunks, whose codes go to codes[0]
+// and codes[1] (two words each; INT4 one). Every lane gets (scale, zero).
+// Called by whole warps.
+template <int KVT, int kLanes>
+__device__ __forceinline__ float2 quantise_lanes(float (&x)[16], uint32_t (&codes)[2][2]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = __fadd_rn(x[e], 0.0f);
+  codes[0][0] = codes[0][1] = codes[1][0] = codes[1][1] = 0;
+  if constexpr (KVT == PA_KV_FP8_PER_TOKEN) {
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = __fdiv_rn(amax, 448.0f);
+    if (s != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 2)
+        codes[e / 8][e / 4 % 2] |=
+            f32x2_to_e4m3x2(__fdiv_rn(x[e], s), __fdiv_rn(x[e + 1], s)) << (8 * (e % 4));
+    }
+    return make_float2(s, 0.f);
+  } else {
+    constexpr float kTop = KVT == PA_KV_U4_PER_TOKEN ? 15.0f : 255.0f;
+    constexpr int kBits = KVT == PA_KV_U4_PER_TOKEN ? 4 : 8;
+    constexpr int kPerWord = 32 / kBits;
+    float mn = x[0], mx = x[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) {
+      mn = fminf(mn, x[e]);
+      mx = fmaxf(mx, x[e]);
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    const float s = __fdiv_rn(__fsub_rn(mx, mn), kTop);
+    if (s != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float r = rintf(__fdiv_rn(__fsub_rn(x[e], mn), s));
+        r = fminf(fmaxf(r, 0.0f), kTop);
+        codes[e / 8][e % 8 / kPerWord] |= static_cast<uint32_t>(r) << (kBits * (e % kPerWord));
+      }
+    }
+    return make_float2(s, mn);
+  }
+}
+
 }  // namespace
 }  // namespace pa
