@@ -38,7 +38,7 @@ NOMINAL_HBM_GBS = 7700.0   # B200 (HGX) specification figure, for context only
 # every source file the decode kernel is compiled from: a recorded ncu traffic
 # figure is used only for the exact sources it was captured from
 KERNEL_SRCS = [os.path.join(ROOT, "paged_kv_cache_466_b200", "csrc", f)
-               for f in ("decode.cu", "pa_device.cuh", "pa_quant.cuh", "pa_internal.h")] + \
+               for f in ("decode.cu", "decode_kernel.cuh", "pa_device.cuh", "pa_quant.cuh", "pa_internal.h")] + \
               [os.path.join(ROOT, "include", "pagedattn.h")]
 
 

@@ -359,6 +359,54 @@ pa_status_t pa_decode_append(const pa_kv_pool_t *pool, const void *q,
                              int32_t num_splits, int32_t *d_err, void *stream);
 
 /*
+ * Changes to the scores of Eq. 1 (the pages have none of them; models of the
+ * same shapes do). With x = scale * q_i . k_j, in this order:
+ *   softcap > 0  : x = softcap * tanh(x / softcap)
+ *   alibi_slopes : x = x - alibi_slopes[query head] * |i - j|, i and j being the
+ *                  cache positions of the query's token and of the key
+ * and key j takes part for query i only if
+ *   doc_begin_i <= j  and  (j <= i or j < prefix_end_i)  and  j < context length.
+ * A query that sees no key gets out = 0. Keys and values that some query of a
+ * call sees must be finite, also for its queries that do not see them.
+ */
+typedef struct {
+  float softcap;               /* >= 0; 0: scores are not capped                 */
+  const float *alibi_slopes;   /* (device) fp32 [num_q_heads], or NULL           */
+  const int32_t *doc_begin;    /* (device) int32, one per query token: the first
+                                  position of its document (a sequence may hold
+                                  several documents one after another); NULL: 0  */
+  const int32_t *prefix_end;   /* (device) int32, one per query token: positions
+                                  below it are seen even where they come later
+                                  (a prompt's prefix, an image); NULL: none      */
+} pa_score_t;
+
+/*
+ * pa_decode_scored — one decode step with the scores changed by `score`, and,
+ * in the same launch, optionally the rotation and the cache write of the step.
+ *   score    : as above, one query token per sequence: doc_begin is
+ *              [num_seqs]; prefix_end is not read (nothing comes later than the
+ *              newest token); NULL: no change
+ *   rope     : rotates q and k_new (pa_rope_t), each rounded to bf16, before
+ *              anything else; NULL: both are used as they are
+ *   rope_pos : (device) int32 [num_axes][num_seqs]; NULL: context_lens[b] - 1 on
+ *              every axis. A position outside [0, table_len) flags
+ *              PA_DERR_BAD_POS; that sequence stores nothing and gets out = 0
+ *   k_new, v_new : as for pa_decode_append, or both NULL: nothing is written
+ * Other arguments, the workspace and the split count as for pa_decode_append;
+ * with every change NULL the result is pa_decode_append's (or pa_decode's),
+ * bit for bit. With rope, the stored row and the result are those of
+ * pa_kv_append_rope followed by a call without rope, k_new and v_new.
+ */
+pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
+                             const pa_rope_t *rope, const void *q, const void *k_new,
+                             const void *v_new, const int32_t *rope_pos,
+                             int32_t num_seqs, int32_t num_q_heads,
+                             const int32_t *block_tables, int32_t max_pages,
+                             const int32_t *context_lens, float scale, float *out,
+                             void *workspace, size_t workspace_bytes,
+                             int32_t num_splits, int32_t *d_err, void *stream);
+
+/*
  * pa_decode_shared_prefix — cascade decode for a batch whose requests all
  * begin with the same prompt prefix stored once in shared pages
  * ("KV-Cache Optimization Techniques", section "Prefix Caching", Eq. 2).

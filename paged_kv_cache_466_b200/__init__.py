@@ -20,6 +20,9 @@ Entry points (same names as the C ABI, see include/pagedattn.h):
                            then the paged decode of each request's own tokens
 * ``pa_decode_window``   — decode over attention sinks + the last w tokens
                            (StreamingLLM / sliding window); evicted pages unread
+* ``pa_decode_scored``   — a decode step whose scores are capped by a tanh, biased
+                           by distance or kept inside a document, optionally with
+                           rotary positions and the cache write in the same launch
 * ``pa_decode_noalloc``  — pa_decode without a caller workspace, for callers
                            that cannot allocate device memory (the scratch is
                            a fixed-size array owned by the library)
@@ -41,9 +44,9 @@ from ._lib import (PA_DERR_BAD_CTX, PA_DERR_BAD_PAGE, PA_DERR_BAD_POS, PA_DERR_B
                    PA_STEP_NEWEST_PER_SEQ,
                    PA_DERR_TIMEOUT,
                    PA_KV_BF16, PA_KV_FP8_PER_TOKEN, PA_KV_U4_PER_TOKEN, PA_KV_U8_PER_TOKEN,
-                   PagedAttnError, pa_kv_pool_t, pa_rope_t)
+                   PagedAttnError, pa_kv_pool_t, pa_rope_t, pa_score_t)
 
-__all__ = ["KVPool", "Rope", "pa_kv_append", "pa_kv_append_rope", "pa_decode", "pa_decode_append", "pa_decode_noalloc", "pa_splitkv_reduce",
+__all__ = ["KVPool", "Rope", "pa_kv_append", "pa_kv_append_rope", "pa_decode", "pa_decode_append", "pa_decode_scored", "pa_decode_noalloc", "pa_splitkv_reduce",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_bytes",
            "pa_decode_window", "pa_decode_window_workspace_bytes",
            "pa_decode_range", "pa_decode_range_workspace_bytes", "pa_merge_partials",
@@ -374,6 +377,80 @@ def pa_decode_append(pool: KVPool, q: torch.Tensor, k_new: torch.Tensor, v_new: 
                                       float(scale), _ptr(out), _ptr(workspace), ws_bytes,
                                       num_splits, _ptr(d_err), _stream(stream))
     _lib.check(st, "pa_decode_append")
+    return out
+
+
+def _score(softcap: float, alibi_slopes: Optional[torch.Tensor], hq: int,
+           doc_begin: Optional[torch.Tensor], prefix_end: Optional[torch.Tensor], tokens: int,
+           device) -> pa_score_t:
+    """The score changes of pa_prefill and pa_decode_scored as the C struct."""
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", torch.float32, device)
+        if alibi_slopes.numel() != hq:
+            raise ValueError(f"alibi_slopes must hold one slope per query head ({hq})")
+    for t, name in ((doc_begin, "doc_begin"), (prefix_end, "prefix_end")):
+        if t is not None:
+            _need(t, name, torch.int32, device)
+            if t.numel() != tokens:
+                raise ValueError(f"{name} must hold one position per query token ({tokens})")
+    return pa_score_t(float(softcap), _ptr(alibi_slopes), _ptr(doc_begin), _ptr(prefix_end))
+
+
+def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, scale: float, softcap: float = 0.0,
+                     alibi_slopes: Optional[torch.Tensor] = None,
+                     doc_begin: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                     rope_pos: Optional[torch.Tensor] = None,
+                     k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+                     d_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One decode step, q [B, Hq, D] bf16 -> out [B, Hq, D] fp32, with the scores
+    capped (``softcap`` > 0), biased by -``alibi_slopes``[head] x distance, and
+    the keys before ``doc_begin`` [B] left out. With ``rope``, q and k_new are
+    rotated first (by ``rope_pos`` int32 [num_axes, B], default the newest
+    token's position); with k_new / v_new [B, Hkv, D] the newest token's row is
+    stored as pa_decode_append does. The workspace is pa_decode's."""
+    dev = pool.device
+    _need_device(dev, "pa_decode_scored", d_err)
+    _need(q, "q", torch.bfloat16, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(context_lens, "context_lens", torch.int32, dev)
+    B, Hq, D = q.shape
+    if D != pool.head_dim or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("pa_decode_scored: shape mismatch")
+    if (k_new is None) != (v_new is None):
+        raise ValueError("pa_decode_scored: k_new and v_new are given together or not at all")
+    if k_new is not None:
+        _need(k_new, "k_new", torch.bfloat16, dev)
+        _need(v_new, "v_new", torch.bfloat16, dev)
+        if tuple(k_new.shape) != (B, pool.num_kv_heads, D) or k_new.shape != v_new.shape:
+            raise ValueError("pa_decode_scored: shape mismatch")
+    if rope is not None and rope.table.device != dev:
+        raise ValueError(f"the rotation's table must be on {dev}, got {rope.table.device}")
+    if rope_pos is not None:
+        _need(rope_pos, "rope_pos", torch.int32, dev)
+        if rope is None or rope_pos.numel() != rope.num_axes * B:
+            raise ValueError("pa_decode_scored: rope_pos must be [num_axes, sequences] of a rope")
+    score = _score(softcap, alibi_slopes, Hq, doc_begin, None, B, dev)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float32, dev)
+    if tuple(out.shape) != (B, Hq, D):
+        raise ValueError("pa_decode_scored: out must be [B, Hq, D]")
+    max_pages = block_tables.shape[1]
+    if workspace is None:
+        need = pa_decode_workspace_bytes(B, Hq, D,
+                                         pa_decode_num_splits(pool, B, max_pages, num_splits))
+        if need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _lib.load().pa_decode_scored(
+        ctypes.byref(pool.c), ctypes.byref(score), None if rope is None else ctypes.byref(rope.c),
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(rope_pos), B, Hq, _ptr(block_tables), max_pages,
+        _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, num_splits,
+        _ptr(d_err), _stream(stream))
+    _lib.check(st, "pa_decode_scored")
     return out
 
 

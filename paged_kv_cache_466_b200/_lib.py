@@ -59,10 +59,20 @@ class pa_rope_t(ctypes.Structure):
     ]
 
 
+class pa_score_t(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("doc_begin", ctypes.c_void_p),
+        ("prefix_end", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _POOL = ctypes.POINTER(pa_kv_pool_t)
 _ROPE = ctypes.POINTER(pa_rope_t)
+_SCORE = ctypes.POINTER(pa_score_t)
 _L = ctypes.c_int64
 
 SIGNATURES = {
@@ -74,6 +84,8 @@ SIGNATURES = {
     "pa_decode_auto_splits": (_I, [_I, _I, _I, _I]),
     "pa_decode_append": (_I, [_POOL, _P, _P, _P, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P,
                               ctypes.c_size_t, _I, _P, _P]),
+    "pa_decode_scored": (_I, [_POOL, _SCORE, _ROPE, _P, _P, _P, _P, _I, _I, _P, _I, _P,
+                              ctypes.c_float, _P, _P, ctypes.c_size_t, _I, _P, _P]),
     "pa_decode_append_lens": (_I, [_POOL, _P, _P, _P, _I, _I, _P, _I, _P, _P, ctypes.c_float, _P, _P,
                               ctypes.c_size_t, _I, _P, _P]),
     "pa_decode_plan_splits": (_I, [ctypes.c_int64, _I, _I, _I, _I, _I]),

@@ -479,7 +479,7 @@ pa_status_t decode_impl(const pa_kv_pool_t *pool, const void *q, int32_t num_seq
                         const int32_t *context_lens, float scale, float *out, void *workspace,
                         size_t workspace_bytes, int32_t num_splits, int32_t *d_err,
                         void *stream, const void *k_new, const void *v_new,
-                        const int32_t *host_lens = nullptr) {
+                        const int32_t *host_lens = nullptr, ScoredArgs *scored = nullptr) {
   g_last_error.clear();
   pa_status_t st = check_pool(pool);
   if (st != PA_OK) return st;
@@ -572,6 +572,12 @@ pa_status_t decode_impl(const pa_kv_pool_t *pool, const void *q, int32_t num_seq
   a.ordered = ordered;
   if (ordered)
     for (int i = 0; i < num_seqs; ++i) a.order[i] = (uint8_t)order[i];
+  if (scored != nullptr) {
+    static_cast<DecodeArgs &>(*scored) = a;
+    return cuda_status(launch_decode_scored(pool->head_dim, pool->page_size, pool->dtype, *scored,
+                                            static_cast<cudaStream_t>(stream)),
+                       "pa_decode_scored launch");
+  }
   return cuda_status(launch_decode(pool->head_dim, pool->page_size, pool->dtype, a,
                                    static_cast<cudaStream_t>(stream)),
                      k_new ? "pa_decode_append launch" : "pa_decode launch");
@@ -621,6 +627,59 @@ pa_status_t pa_decode_append_lens(const pa_kv_pool_t *pool, const void *q, const
                      scale, out, workspace, workspace_bytes, num_splits, d_err, stream,
                      num_seqs > 0 ? k_new : nullptr, num_seqs > 0 ? v_new : nullptr,
                      host_context_lens);
+}
+
+namespace {
+
+pa_status_t check_score(const pa_score_t *score) {
+  if (score == nullptr) return PA_OK;
+  if (!(score->softcap >= 0.f) || score->softcap > 3.0e38f)
+    return fail(PA_ERR_INVALID_ARG, "softcap=%g (0 or a positive finite number)",
+                (double)score->softcap);
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
+                             const pa_rope_t *rope, const void *q, const void *k_new,
+                             const void *v_new, const int32_t *rope_pos, int32_t num_seqs,
+                             int32_t num_q_heads, const int32_t *block_tables, int32_t max_pages,
+                             const int32_t *context_lens, float scale, float *out,
+                             void *workspace, size_t workspace_bytes, int32_t num_splits,
+                             int32_t *d_err, void *stream) {
+  g_last_error.clear();
+  pa_status_t st = check_pool(pool);
+  if (st == PA_OK) st = check_score(score);
+  if (st == PA_OK && rope != nullptr) st = check_rope(rope, pool->head_dim);
+  if (st != PA_OK) return st;
+  if ((k_new == nullptr) != (v_new == nullptr))
+    return fail(PA_ERR_INVALID_ARG, "k_new and v_new are given together or not at all");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16))
+    return fail(PA_ERR_INVALID_ARG, "k_new/v_new must be 16-byte aligned");
+  if (rope_pos != nullptr && rope == nullptr)
+    return fail(PA_ERR_INVALID_ARG, "rope_pos without rope");
+  ScoredArgs sa;
+  if (score != nullptr) {
+    if (score->softcap > 0.f) {
+      sa.cap_l2 = score->softcap * 1.4426950408889634f;
+      sa.inv_cap = 1.f / sa.cap_l2;
+    }
+    sa.slopes = score->alibi_slopes;
+    sa.doc_begin = score->doc_begin;
+  }
+  if (rope != nullptr) {
+    sa.table = rope->table;
+    sa.rope_pos = rope_pos;
+    sa.table_len = rope->table_len;
+    sa.rot = rope->rotary_dim;
+    sa.interleaved = rope->interleaved;
+    sa.num_axes = rope->num_axes;
+    std::memcpy(sa.axis_of_pair, rope->axis_of_pair, sizeof sa.axis_of_pair);
+  }
+  return decode_impl(pool, q, num_seqs, num_q_heads, block_tables, max_pages, context_lens,
+                     scale, out, workspace, workspace_bytes, num_splits, d_err, stream,
+                     num_seqs > 0 ? k_new : nullptr, num_seqs > 0 ? v_new : nullptr, nullptr, &sa);
 }
 
 // ---------------------------------------------------------------- shared prefix

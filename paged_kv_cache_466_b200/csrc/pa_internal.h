@@ -72,6 +72,22 @@ struct DecodeArgs {
   const unsigned char *v_new = nullptr;
 };
 
+// pa_decode_scored: a decode with changed scores and, optionally, the rotation
+// of the query and of the new key (fields of pa_rope_t).
+struct ScoredArgs : DecodeArgs {
+  float cap_l2 = 0.f;   // softcap * log2(e); 0: not capped
+  float inv_cap = 0.f;  // 1 / cap_l2
+  const float *slopes = nullptr;       // [hq]
+  const int32_t *doc_begin = nullptr;  // [B]
+  const float *table = nullptr;        // no rotation when null
+  const int32_t *rope_pos = nullptr;   // [num_axes][B]; null: ctx - 1
+  int32_t table_len = 0;
+  int32_t rot = 0;
+  int32_t interleaved = 0;
+  int32_t num_axes = 0;
+  uint8_t axis_of_pair[64];
+};
+
 struct PrefixArgs {
   const void *k_pool;
   const void *v_pool;
@@ -103,6 +119,8 @@ int prefix_tile_tokens();
 
 cudaError_t launch_decode(int D, int P, int kv_dtype, const DecodeArgs &a,
                           cudaStream_t stream);
+cudaError_t launch_decode_scored(int D, int P, int kv_dtype, const ScoredArgs &a,
+                                 cudaStream_t stream);
 // CTAs of the decode kernel for (D, P, kv_dtype) that fit on one SM.
 int decode_ctas_per_sm(int D, int P, int kv_dtype);
 
