@@ -407,6 +407,47 @@ pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
                              int32_t num_splits, int32_t *d_err, void *stream);
 
 /*
+ * pa_prefill — Eq. 1 for many query tokens per sequence (a prompt, a chunk of
+ * one behind cached tokens, draft tokens), with the scores changed by `score`.
+ * The keys and values of the query tokens are already in the cache
+ * (pa_kv_append or pa_kv_append_rope): sequence b's query tokens are the last
+ * ones of its context_lens[b] tokens, so query token i of sequence b stands at
+ * position context_lens[b] - (q_begin[b + 1] - q_begin[b]) + (i - q_begin[b]).
+ *   q        : (device) bf16 [num_tokens][num_q_heads][head_dim]
+ *   q_begin  : (device) int32 [num_seqs + 1], ascending, within [0, num_tokens]:
+ *              sequence b's query tokens are rows q_begin[b] .. q_begin[b + 1] - 1
+ *              (none is allowed); a sequence whose entries are not so is
+ *              clamped into range and flagged PA_DERR_BAD_SEQ
+ *   context_lens : (device) int32 [num_seqs]; one that is below the sequence's
+ *              query tokens or past its table flags PA_DERR_BAD_CTX and its
+ *              queries see nothing (out = 0)
+ *   score    : doc_begin and prefix_end are [num_tokens]; NULL: causal attention
+ *   out      : (device) bf16 [num_tokens][num_q_heads][head_dim]; rows outside
+ *              q_begin[0] .. q_begin[num_seqs] - 1 are left as they were
+ *   lse_out  : (device) fp32 [num_tokens][num_q_heads], natural log of the sum
+ *              of exp(x) over the visible keys (-inf: none), or NULL
+ *   num_splits : 0 = automatic: the keys are split over CTAs when there are few
+ *              query rows, and the partials merged by a second launch
+ *   workspace : (device) >= pa_prefill_workspace_bytes(...) bytes, 256-byte
+ *              aligned; NULL when that is 0. May be shared with other entry
+ *              points (see pa_decode_workspace_bytes); the calls must not overlap
+ * All cache formats. A page id outside the pool is flagged PA_DERR_BAD_PAGE and
+ * its tokens are left out. The softmax weights are rounded to bf16 for the
+ * second product, sums and statistics are fp32. Deterministic.
+ */
+size_t pa_prefill_workspace_bytes(const pa_kv_pool_t *pool, int32_t num_tokens,
+                                  int32_t num_seqs, int32_t num_q_heads,
+                                  int32_t max_pages, int32_t num_splits);
+
+pa_status_t pa_prefill(const pa_kv_pool_t *pool, const pa_score_t *score, const void *q,
+                       int32_t num_tokens, int32_t num_q_heads, const int32_t *q_begin,
+                       int32_t num_seqs, const int32_t *block_tables,
+                       int32_t max_pages, const int32_t *context_lens, float scale,
+                       void *out, float *lse_out, void *workspace,
+                       size_t workspace_bytes, int32_t num_splits, int32_t *d_err,
+                       void *stream);
+
+/*
  * pa_decode_shared_prefix — cascade decode for a batch whose requests all
  * begin with the same prompt prefix stored once in shared pages
  * ("KV-Cache Optimization Techniques", section "Prefix Caching", Eq. 2).

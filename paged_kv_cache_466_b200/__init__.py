@@ -20,6 +20,9 @@ Entry points (same names as the C ABI, see include/pagedattn.h):
                            then the paged decode of each request's own tokens
 * ``pa_decode_window``   — decode over attention sinks + the last w tokens
                            (StreamingLLM / sliding window); evicted pages unread
+* ``pa_prefill``         — attention of many query tokens per sequence (prompts,
+                           chunks, drafts) over the paged cache, with the same
+                           changes of the scores as ``pa_decode_scored``
 * ``pa_decode_scored``   — a decode step whose scores are capped by a tanh, biased
                            by distance or kept inside a document, optionally with
                            rotary positions and the cache write in the same launch
@@ -46,7 +49,8 @@ from ._lib import (PA_DERR_BAD_CTX, PA_DERR_BAD_PAGE, PA_DERR_BAD_POS, PA_DERR_B
                    PA_KV_BF16, PA_KV_FP8_PER_TOKEN, PA_KV_U4_PER_TOKEN, PA_KV_U8_PER_TOKEN,
                    PagedAttnError, pa_kv_pool_t, pa_rope_t, pa_score_t)
 
-__all__ = ["KVPool", "Rope", "pa_kv_append", "pa_kv_append_rope", "pa_decode", "pa_decode_append", "pa_decode_scored", "pa_decode_noalloc", "pa_splitkv_reduce",
+__all__ = ["KVPool", "Rope", "pa_kv_append", "pa_kv_append_rope", "pa_decode", "pa_decode_append", "pa_decode_scored", "pa_decode_noalloc",
+           "pa_prefill", "pa_prefill_workspace_bytes", "pa_splitkv_reduce",
            "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_bytes",
            "pa_decode_window", "pa_decode_window_workspace_bytes",
            "pa_decode_range", "pa_decode_range_workspace_bytes", "pa_merge_partials",
@@ -451,6 +455,60 @@ def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
         _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), ws_bytes, num_splits,
         _ptr(d_err), _stream(stream))
     _lib.check(st, "pa_decode_scored")
+    return out
+
+
+def pa_prefill_workspace_bytes(pool: KVPool, num_tokens: int, num_seqs: int, num_q_heads: int,
+                               max_pages: int, num_splits: int = 0) -> int:
+    return int(_lib.load().pa_prefill_workspace_bytes(ctypes.byref(pool.c), num_tokens, num_seqs,
+                                                      num_q_heads, max_pages, num_splits))
+
+
+def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_tables: torch.Tensor,
+               context_lens: torch.Tensor, scale: float, softcap: float = 0.0,
+               alibi_slopes: Optional[torch.Tensor] = None,
+               doc_begin: Optional[torch.Tensor] = None,
+               prefix_end: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               lse_out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+               d_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the query tokens q [N, Hq, D] bf16 of a ragged batch over the
+    paged cache -> out [N, Hq, D] bf16. Sequence b's tokens are rows
+    ``q_begin[b] : q_begin[b + 1]`` and the last of its ``context_lens[b]`` cached
+    tokens; causal unless ``prefix_end`` [N] (positions below it are seen by that
+    token in any case) says otherwise, from ``doc_begin`` [N] on. Scores are
+    capped with ``softcap`` > 0 and biased by -``alibi_slopes``[head] x distance.
+    ``lse_out`` fp32 [N, Hq] also receives the log-sum-exps."""
+    dev = pool.device
+    _need_device(dev, "pa_prefill", d_err)
+    _need(q, "q", torch.bfloat16, dev)
+    _need(q_begin, "q_begin", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _need(context_lens, "context_lens", torch.int32, dev)
+    N, Hq, D = q.shape
+    B, max_pages = block_tables.shape
+    if D != pool.head_dim or context_lens.numel() != B or q_begin.numel() != B + 1:
+        raise ValueError("pa_prefill: shape mismatch")
+    score = _score(softcap, alibi_slopes, Hq, doc_begin, prefix_end, N, dev)
+    if out is None:
+        out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev)
+    if tuple(out.shape) != (N, Hq, D):
+        raise ValueError("pa_prefill: out must be [N, Hq, D]")
+    if lse_out is not None:
+        _need(lse_out, "lse_out", torch.float32, dev)
+        if tuple(lse_out.shape) != (N, Hq):
+            raise ValueError("pa_prefill: lse_out must be [N, Hq]")
+    if workspace is None:
+        need = pa_prefill_workspace_bytes(pool, N, B, Hq, max_pages, num_splits)
+        if need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = _lib.load().pa_prefill(
+        ctypes.byref(pool.c), ctypes.byref(score), _ptr(q), N, Hq, _ptr(q_begin), B,
+        _ptr(block_tables), max_pages, _ptr(context_lens), float(scale), _ptr(out), _ptr(lse_out),
+        _ptr(workspace), ws_bytes, num_splits, _ptr(d_err), _stream(stream))
+    _lib.check(st, "pa_prefill")
     return out
 
 

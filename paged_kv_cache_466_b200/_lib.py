@@ -86,6 +86,9 @@ SIGNATURES = {
                               ctypes.c_size_t, _I, _P, _P]),
     "pa_decode_scored": (_I, [_POOL, _SCORE, _ROPE, _P, _P, _P, _P, _I, _I, _P, _I, _P,
                               ctypes.c_float, _P, _P, ctypes.c_size_t, _I, _P, _P]),
+    "pa_prefill_workspace_bytes": (ctypes.c_size_t, [_POOL, _I, _I, _I, _I, _I]),
+    "pa_prefill": (_I, [_POOL, _SCORE, _P, _I, _I, _P, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P,
+                        ctypes.c_size_t, _I, _P, _P]),
     "pa_decode_append_lens": (_I, [_POOL, _P, _P, _P, _I, _I, _P, _I, _P, _P, ctypes.c_float, _P, _P,
                               ctypes.c_size_t, _I, _P, _P]),
     "pa_decode_plan_splits": (_I, [ctypes.c_int64, _I, _I, _I, _I, _I]),

@@ -682,6 +682,127 @@ pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
                      num_seqs > 0 ? k_new : nullptr, num_seqs > 0 ? v_new : nullptr, nullptr, &sa);
 }
 
+// ---------------------------------------------------------------------- prefill
+namespace {
+
+// Key splits of pa_prefill: with fewer (256-row block, KV head) units than
+// SMs, as many as fill the SMs once, each of at least four 128-key tiles.
+// The blocks are estimated from the token count, the keys from the table width.
+int prefill_splits(const pa_kv_pool_t *pool, int n, int B, int hq, int max_pages, int requested) {
+  const long long tiles = ((long long)max_pages * pool->page_size + 127) / 128;
+  long long S = requested;
+  if (requested == 0) {
+    const long long rows = (long long)n * (hq / pool->num_kv_heads);
+    const long long blocks = std::max<long long>((rows + 255) / 256, std::min(n, B));
+    const long long units = std::max<long long>(blocks * pool->num_kv_heads, 1);
+    S = std::min<long long>(device_sm_count() / units, tiles / 4);
+  }
+  S = std::min<long long>(S, std::min<long long>(tiles, kMaxSplits));
+  return S < 1 ? 1 : (int)S;
+}
+
+pa_status_t check_prefill(const pa_kv_pool_t *pool, int n, int B, int hq, int max_pages, int splits) {
+  pa_status_t st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (n < 0 || B < 0 || hq <= 0 || max_pages <= 0 || splits < 0)
+    return fail(PA_ERR_INVALID_ARG,
+                "num_tokens=%d num_seqs=%d num_q_heads=%d max_pages=%d num_splits=%d", n, B, hq,
+                max_pages, splits);
+  if (hq % pool->num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads=%d is not a multiple of num_kv_heads=%d", hq,
+                pool->num_kv_heads);
+  if (hq / pool->num_kv_heads > kMaxGroup)
+    return fail(PA_ERR_UNSUPPORTED, "GQA group %d > %d query heads per KV head",
+                hq / pool->num_kv_heads, kMaxGroup);
+  if (n > (1 << 24) || B > 65535 || hq > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "at most 2^24 tokens, 65535 sequences and 65535 heads");
+  if ((long long)max_pages * pool->page_size > (1LL << 30))
+    return fail(PA_ERR_UNSUPPORTED, "max_pages * page_size too large");
+  return PA_OK;
+}
+
+}  // namespace
+
+size_t pa_prefill_workspace_bytes(const pa_kv_pool_t *pool, int32_t num_tokens, int32_t num_seqs,
+                                  int32_t num_q_heads, int32_t max_pages, int32_t num_splits) {
+  if (check_prefill(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits) != PA_OK) return 0;
+  const int S = prefill_splits(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits);
+  if (S <= 1 || num_tokens == 0) return 0;
+  const size_t parts = (size_t)num_tokens * num_q_heads * S * sizeof(float);
+  return workspace_for(align256(parts * pool->head_dim) + align256(parts), 0);
+}
+
+pa_status_t pa_prefill(const pa_kv_pool_t *pool, const pa_score_t *score, const void *q,
+                       int32_t num_tokens, int32_t num_q_heads, const int32_t *q_begin,
+                       int32_t num_seqs, const int32_t *block_tables, int32_t max_pages,
+                       const int32_t *context_lens, float scale, void *out, float *lse_out,
+                       void *workspace, size_t workspace_bytes, int32_t num_splits, int32_t *d_err,
+                       void *stream) {
+  g_last_error.clear();
+  pa_status_t st =
+      check_prefill(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits);
+  if (st == PA_OK) st = check_score(score);
+  if (st != PA_OK) return st;
+  if (!(scale == scale)) return fail(PA_ERR_INVALID_ARG, "scale is NaN");
+  if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!q || !q_begin || !block_tables || !context_lens || !out)
+    return fail(PA_ERR_INVALID_ARG, "q, q_begin, block_tables, context_lens and out are required");
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail(PA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const int S = prefill_splits(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits);
+  const size_t parts = (size_t)num_tokens * num_q_heads * S * sizeof(float);
+  const size_t o_bytes = align256(parts * pool->head_dim);
+  if (S > 1) {
+    if (workspace == nullptr || !workspace_fits(workspace_bytes, o_bytes + align256(parts), 0))
+      return fail(PA_ERR_WORKSPACE, "workspace: need %zu bytes for %d splits, got %zu",
+                  workspace_for(o_bytes + align256(parts), 0), S,
+                  workspace == nullptr ? (size_t)0 : workspace_bytes);
+    if (!aligned(workspace, 256))
+      return fail(PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  if (prefill_blocks(num_tokens, num_seqs, num_q_heads / pool->num_kv_heads) *
+          pool->num_kv_heads * S > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "too many blocks for one launch");
+  PrefillArgs a = {};
+  a.k_pool = pool->k_pool;
+  a.v_pool = pool->v_pool;
+  a.k_sz = pool->k_sz;
+  a.v_sz = pool->v_sz;
+  a.num_pages = pool->num_pages;
+  a.hkv = pool->num_kv_heads;
+  a.P = pool->page_size;
+  a.q = q;
+  a.n = num_tokens;
+  a.B = num_seqs;
+  a.hq = num_q_heads;
+  a.q_begin = q_begin;
+  a.block_tables = block_tables;
+  a.max_pages = max_pages;
+  a.ctx = context_lens;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (score != nullptr) {
+    if (score->softcap > 0.f) {
+      a.cap_l2 = score->softcap * 1.4426950408889634f;
+      a.inv_cap = 1.f / a.cap_l2;
+    }
+    a.slopes = score->alibi_slopes;
+    a.doc_begin = score->doc_begin;
+    a.prefix_end = score->prefix_end;
+  }
+  a.out = out;
+  a.lse_out = lse_out;
+  a.S = S;
+  if (S > 1) {
+    // past the split counters that other entry points keep in a shared workspace
+    char *base = static_cast<char *>(workspace) + counter_region(workspace_bytes);
+    a.o_part = reinterpret_cast<float *>(base);
+    a.lse_part = reinterpret_cast<float *>(base + o_bytes);
+  }
+  a.d_err = d_err;
+  return cuda_status(launch_prefill(pool->head_dim, pool->dtype, a, static_cast<cudaStream_t>(stream)),
+                     "pa_prefill launch");
+}
+
 // ---------------------------------------------------------------- shared prefix
 namespace {
 

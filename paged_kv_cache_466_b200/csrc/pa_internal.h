@@ -175,6 +175,42 @@ struct AppendRopeArgs {
 cudaError_t launch_append_rope(int D, int kv_dtype, const AppendRopeArgs &a, bool interleaved,
                                cudaStream_t stream);
 
+// pa_prefill.
+struct PrefillArgs {
+  CUtensorMap tmk, tmv;  // bf16 pools as [num_pages][Hkv][P][D]; set by the launch
+  const void *k_pool;
+  const void *v_pool;
+  const float *k_sz;
+  const float *v_sz;
+  int32_t num_pages;
+  int32_t hkv;
+  int32_t P;
+  const void *q;  // bf16 [n][hq][D]
+  int32_t n;
+  int32_t B;
+  int32_t hq;
+  const int32_t *q_begin;  // [B + 1]
+  const int32_t *block_tables;
+  int32_t max_pages;
+  const int32_t *ctx;
+  float scale_log2;
+  float cap_l2;   // softcap * log2(e); 0: not capped
+  float inv_cap;  // 1 / cap_l2
+  const float *slopes;
+  const int32_t *doc_begin;
+  const int32_t *prefix_end;
+  void *out;       // bf16 [n][hq][D]
+  float *lse_out;  // [n][hq] or null
+  int32_t S;       // splits of the keys; S > 1 writes partials, merged by a second launch
+  float *o_part;   // [n][hq][S][D]
+  float *lse_part; // [n][hq][S]
+  int32_t *d_err;
+};
+
+cudaError_t launch_prefill(int D, int kv_dtype, const PrefillArgs &a, cudaStream_t stream);
+// Most 256-row blocks that n query tokens of B sequences can make per KV head.
+long long prefill_blocks(int n, int B, int G);
+
 cudaError_t launch_validate_tables(const int32_t *block_tables, int32_t B,
                                    int32_t max_pages, const int32_t *ctx,
                                    int32_t num_pages, int32_t page_size,

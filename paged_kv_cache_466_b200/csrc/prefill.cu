@@ -1,0 +1,793 @@
+// Attention of many query tokens per sequence over the paged cache
+// (pa_prefill): prompts, chunks of prompts, draft tokens, on the
+// fifth-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// Eq. 1 of "KV-Cache Optimization Techniques", section "PagedAttention
+// (vLLM)", for every query token of a ragged batch, with an online softmax:
+// per KV head, the (token, query head) rows of a sequence that read that head
+// are packed (row r is token r / G, head r % G), so the K and V tiles are read
+// once for the whole group. A CTA takes 256 rows as two tiles of 128 and walks
+// the 128-key tiles between the first and the last key any of its rows sees,
+// from the last to the first.
+//
+//   warps 0-3, 4-7   softmax of row tile 0, 1: thread = row = TMEM lane
+//   warp 8           issues the MMAs (one thread)
+//   warps 9-11       bring K and V tiles into shared memory: bf16 pools by TMA
+//                    (one box per page and 64 columns), quantised pools by
+//                    loads and exact conversion of the codes to bf16
+//
+//   S[128 x 128] = Q K^T  : Q and K K-major, 128-byte-swizzled in shared memory
+//   O[128 x D]  += P V    : P from tensor memory (bf16, over the scores' own
+//                           columns), V as the page rows lie (MN-major)
+//
+// PV of tile k and S of tile k + 1 of one row tile are issued together, while
+// the other row tile is in its softmax, and one commit covers both: a thread
+// that has seen it may read the new scores and may rescale O.
+//
+// Quantised pools (x = s c + z per row): codes reach the MMA exactly (INT8 as
+// c - 128, INT4 as c - 8, E4M3 as it is); q.x = s (q.c) + z sum(q) and
+// sum p x = sum (p s) c + sum p z are applied once per score.
+//
+// P is rounded to bf16 (half a step, 2^-9 of each weight's binade) as the
+// output is; the denominator and all statistics stay fp32.
+#include <atomic>
+#include <cmath>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kRescaleLog2 = 8.0f;  // raise the running max only past this
+constexpr int kTile = 128;            // query rows of a tile, and keys of a tile
+constexpr int kCtaRows = 2 * kTile;
+constexpr int kThreads = 384;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp0 = 9;
+constexpr int kLoadThreads = 96;
+constexpr int kTmemCols = 512;
+// registers per thread after the split of the launch's 168 * 384
+constexpr int kLaunchRegs = 168;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads, "register split");
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s (a tile takes microseconds)
+
+template <int D, int KVT>
+struct Layout {
+  static constexpr int kQBytes = kTile * D * 2;      // one row tile's queries
+  static constexpr int kSlotBytes = kTile * D * 2;   // one K or V tile, bf16
+  static constexpr int kSlots = KVT == PA_KV_BF16 ? 5 : 4;
+  static constexpr int kQOff = 0;
+  static constexpr int kSlotOff = 2 * kQBytes;
+  // per key (K scale, K zero, V scale, V zero) of the last four tiles
+  static constexpr int kSzOff = kSlotOff + kSlots * kSlotBytes;
+  static constexpr int kSzBytes = KVT == PA_KV_BF16 ? 0 : 4 * kTile * 16;
+  static constexpr int kBarOff = kSzOff + kSzBytes;
+  static constexpr int kBytes = kBarOff + 512 + 1024;  // + alignment slack
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// Shared control block behind the tiles.
+struct Control {
+  uint64_t full[5], empty[5];  // K / V slots
+  uint64_t s_full[2];          // scores of a row tile (and the PV before them) done
+  uint64_t p_full[2];          // P of a row tile stored, O rescaled
+  uint32_t tmem;
+  int32_t dead;                // a bounded wait ran out: everybody stops
+  int32_t seq, blk, q0, qlen, ctx;
+  int32_t lo, hi, rows2;       // first / past-the-last key of any row; row tiles in use
+  uint32_t valid[4];           // per tile (mod 4): valid 16-key blocks
+};
+
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Waits for a phase; gives up after kWaitLimitNs, or at once when another
+// warp has given up.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int32_t *dead) {
+  if (try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (int i = 0; i < (1 << 26); ++i) {
+    if (try_wait(bar, parity)) return true;
+    if ((i & 15) == 15 && (*dead || global_ns() - t0 > kWaitLimitNs)) break;
+  }
+  *dead = 1;
+  return false;
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void proxy_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One page's block of one KV head, 64 columns: [64][P][1][1] of the pool seen
+// as [D][P][Hkv][num_pages]. A page id past the pool reads zeros.
+__device__ __forceinline__ void tma_page(const CUtensorMap *map, uint32_t dst, uint32_t bar, int x,
+                                         int h, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(0), "r"(h), "r"(page)
+      : "memory");
+}
+
+__device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// ---- exact conversions of codes to bf16 pairs ---------------------------------------
+
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two bytes in bits 0..7 and 16..23 -> (c - 128) each: 0x4300 | (c & 127) is
+// 128 + (c & 127); subtracting 128 where bit 7 is set and 256 where it is not
+// leaves c - 128.
+__device__ __forceinline__ uint32_t u8x2_to_bf16(uint32_t w) {
+  return bf16x2_sub((w & 0x007F007Fu) | 0x43004300u, (w & 0x00800080u) ^ 0x43804380u);
+}
+// Two nibbles in bits 0..3 and 16..19 -> c - 8.
+__device__ __forceinline__ uint32_t u4x2_to_bf16(uint32_t w) {
+  return bf16x2_sub((w & 0x000F000Fu) | 0x43004300u, 0x43084308u);
+}
+// Two E4M3 codes in bits 0..7 and 16..23: sign, exponent and mantissa moved
+// into bf16's places read as the value times 2^-120 (subnormals included).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w) {
+  return bf16x2_mul(((w & 0x00800080u) << 8) | ((w & 0x007F007Fu) << 4), 0x7B807B80u);
+}
+
+// 16 codes (8 bytes of INT4, 16 of INT8 / FP8) -> 16 bf16 in element order.
+template <int KVT>
+__device__ __forceinline__ void codes16(const uint32_t *w, uint32_t (&r)[8]) {
+  if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // byte j: elements 2j (low nibble), 2j + 1
+        const uint32_t b = w[i] >> (8 * j);
+        r[4 * i + j] = u4x2_to_bf16((b & 0xFu) | ((b & 0xF0u) << 12));
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __byte_perm(w[i], 0u, 0x4140), hi = __byte_perm(w[i], 0u, 0x4342);
+      r[2 * i] = KVT == PA_KV_FP8_PER_TOKEN ? e4m3x2_to_bf16(lo) : u8x2_to_bf16(lo);
+      r[2 * i + 1] = KVT == PA_KV_FP8_PER_TOKEN ? e4m3x2_to_bf16(hi) : u8x2_to_bf16(hi);
+    }
+  }
+}
+template <int KVT>
+constexpr float kCodeShift = KVT == PA_KV_U8_PER_TOKEN ? 128.f : KVT == PA_KV_U4_PER_TOKEN ? 8.f : 0.f;
+
+// ---- the kernel ----------------------------------------------------------------------
+
+template <int D, int KVT>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  using L = Layout<D, KVT>;
+  constexpr bool kQuant = KVT != PA_KV_BF16;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Control &c = *reinterpret_cast<Control *>(smem + L::kBarOff);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait_primary();
+
+  const int h = blockIdx.x % a.hkv;
+  const int split = blockIdx.x / a.hkv % a.S;
+  const int flat = blockIdx.x / a.hkv / a.S;
+  const int G = a.hq / a.hkv;
+
+  // ---- which sequence and rows: warp 0 adds up the sequences' blocks. Blocks
+  // are taken from the last to the first, so that with causal masks the ones
+  // with most keys start first.
+  if (warp == 0) {
+    auto blocks_of = [&](int b, int &s, int &len) {
+      const int q0 = __ldg(a.q_begin + b), q1 = __ldg(a.q_begin + b + 1);
+      s = max(q0, 0);
+      len = max(min(q1, a.n) - s, 0);
+      if (blockIdx.x == 0 && (q0 < 0 || q1 > a.n || q1 < q0)) flag_error(a.d_err, PA_DERR_BAD_SEQ);
+      return (int)(((long long)len * G + kCtaRows - 1) / kCtaRows);
+    };
+    int total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int s, len;
+      const int nb = b0 + lane < a.B ? blocks_of(b0 + lane, s, len) : 0;
+      total += __reduce_add_sync(0xffffffffu, nb);
+    }
+    if (lane == 0) c.seq = -1;
+    __syncwarp();
+    const int want = total - 1 - flat;
+    if (want >= 0) {
+      int before = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        int s = 0, len = 0;
+        const int nb = b0 + lane < a.B ? blocks_of(b0 + lane, s, len) : 0;
+        int incl = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (want >= before + incl - nb && want < before + incl) {
+          const int b = b0 + lane;
+          c.seq = b;
+          c.blk = want - (before + incl - nb);
+          c.q0 = s;
+          c.qlen = len;
+          int ctx = __ldg(a.ctx + b);
+          if (ctx < len || ctx > a.max_pages * a.P) {  // no such context: sees nothing
+            flag_error(a.d_err, PA_DERR_BAD_CTX);
+            ctx = 0;
+          }
+          c.ctx = ctx;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+        if (want < before) break;
+      }
+    }
+    if (lane == 0) {
+      c.lo = 0x7fffffff;
+      c.hi = 0;
+      c.dead = 0;
+      for (int i = 0; i < 5; ++i) {
+        bar_init(smem_u32(&c.full[i]), kQuant ? kLoadThreads : 1);
+        bar_init(smem_u32(&c.empty[i]), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        bar_init(smem_u32(&c.s_full[i]), 1);
+        bar_init(smem_u32(&c.p_full[i]), kTile);
+      }
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+  }
+  __syncthreads();
+  if (c.seq < 0) return;  // CTA-uniform: past the last block
+  const int b = c.seq, qlen = c.qlen, ctx = c.ctx;
+  const int rows = qlen * G - c.blk * kCtaRows;  // of this CTA; may pass 256
+
+  // ---- this thread's row: what it sees, its query into shared memory
+  int lo = 0, hi = 0x7fffffff;  // an unused row masks nothing
+  int pos = 0;
+  bool row_ok = false;
+  size_t orow = 0;
+  const int sub = warp >> 2;  // row tile of a softmax warp
+  if (tid < kSoftmaxThreads) {
+    row_ok = tid < rows;
+    if (row_ok) {
+      const int r = c.blk * kCtaRows + tid;
+      const int tok = r / G, head = h * G + r % G;
+      orow = (size_t)(c.q0 + tok) * a.hq + head;
+      pos = ctx - qlen + tok;
+      hi = pos + 1;
+      if (a.prefix_end != nullptr) hi = max(hi, __ldg(a.prefix_end + c.q0 + tok));
+      hi = min(hi, ctx);
+      if (a.doc_begin != nullptr) lo = max(__ldg(a.doc_begin + c.q0 + tok), 0);
+      if (hi <= lo) lo = hi = 0;
+    }
+    const unsigned char *src = static_cast<const unsigned char *>(a.q) + orow * D * 2;
+    const uint32_t dst = sbase + L::kQOff + sub * L::kQBytes;
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k)
+      cp_async16(dst + sw128(tid & 127, k, kTile), src + k * 16, row_ok ? 16u : 0u);
+    cp_async_commit();
+    const bool sees = row_ok && hi > lo;
+    const int wlo = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff);
+    const int whi = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
+    if (lane == 0 && whi > 0) {
+      atomicMin(&c.lo, wlo);
+      atomicMax(&c.hi, whi);
+    }
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&c.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  cp_async_wait<0>();
+  proxy_fence();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  // ---- this split's key tiles [t0, t1), walked from t1 - 1 down
+  int t0 = 0, t1 = 0;
+  if (c.hi > 0) {
+    const int f = c.lo / kTile, e = (c.hi + kTile - 1) / kTile;
+    const int per = (e - f + a.S - 1) / a.S;
+    t0 = f + split * per;
+    t1 = min(t0 + per, e);
+    if (t1 < t0) t1 = t0;
+  }
+  const int n = t1 - t0;
+  const int subs = rows > kTile ? 2 : 1;  // row tiles in use
+  const uint32_t tmem = c.tmem;
+  volatile int32_t *dead = &c.dead;
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
+      if (lane == 0 && n > 0) {
+        // ---- MMA issue
+        auto slot_addr = [&](int i) { return sbase + L::kSlotOff + (i % L::kSlots) * L::kSlotBytes; };
+        auto wait_slot = [&](int i) {
+          return wait_bar(smem_u32(&c.full[i % L::kSlots]), (i / L::kSlots) & 1, dead);
+        };
+        auto issue_s = [&](int sb, int k) {
+          const uint32_t q0 = sbase + L::kQOff + sb * L::kQBytes;
+          const uint32_t k0 = slot_addr(2 * k);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+            umma_bf16(tmem + sb * kTile, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024),
+                      instr_desc(kTile, false), kk > 0);
+          }
+        };
+        auto issue_pv = [&](int sb, int k) {
+          const uint32_t v0 = slot_addr(2 * k + 1);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ts(tmem + 2 * kTile + sb * D, tmem + sb * kTile + kk * 8,
+                         smem_desc(v0 + kk * 2048, kTile * 128, 1024), instr_desc(D, true),
+                         k > 0 || kk > 0);
+        };
+        bool ok = wait_slot(0);
+        tc_fence_after();
+        for (int sb = 0; ok && sb < subs; ++sb) {
+          issue_s(sb, 0);
+          umma_commit(smem_u32(&c.s_full[sb]));
+        }
+        if (ok) umma_commit(smem_u32(&c.empty[0]));
+        for (int k = 0; ok && k < n; ++k) {
+          ok = wait_slot(2 * k + 1);
+          if (ok && k + 1 < n) ok = wait_slot(2 * k + 2);
+          for (int sb = 0; ok && sb < subs; ++sb) {
+            ok = wait_bar(smem_u32(&c.p_full[sb]), k & 1, dead);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(sb, k);
+            if (k + 1 < n) issue_s(sb, k + 1);
+            umma_commit(smem_u32(&c.s_full[sb]));
+          }
+          if (ok) {
+            umma_commit(smem_u32(&c.empty[(2 * k + 1) % L::kSlots]));
+            if (k + 1 < n) umma_commit(smem_u32(&c.empty[(2 * k + 2) % L::kSlots]));
+          }
+        }
+      }
+      __syncwarp();
+    } else if constexpr (!kQuant) {
+      // ---- K and V tiles by TMA, one warp: lane = (page of the tile, 64 columns)
+      if (warp == kLoadWarp0 && n > 0) {
+        const int per_tile = kTile / a.P;
+        const int pi = lane % per_tile, half = lane / per_tile;
+        const bool mine = half < D / 64;
+        const uint32_t box = (uint32_t)a.P * 128;
+        bool ok = true;
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          const int tile = t1 - 1 - (i >> 1);
+          const bool is_v = i & 1;
+          const int slot = i % L::kSlots;
+          if (i >= L::kSlots)
+            ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t dst = sbase + L::kSlotOff + slot * L::kSlotBytes;
+          const uint32_t bar = smem_u32(&c.full[slot]);
+          const int tok0 = tile * kTile + pi * a.P;
+          int page = a.num_pages;  // past the pool: zeros
+          bool bad = false;
+          if (tok0 < ctx) {
+            const int id = __ldg(a.block_tables + (size_t)b * a.max_pages + tok0 / a.P);
+            bad = id < 0 || id >= a.num_pages;
+            if (!bad) page = id;
+            if (bad && mine && half == 0 && !is_v) flag_error(a.d_err, PA_DERR_BAD_PAGE);
+          }
+          if (!is_v) {
+            // 16-key blocks of the tile that lie in valid pages
+            const uint32_t m = __ballot_sync(0xffffffffu, !bad && lane < per_tile);
+            uint32_t v = 0;
+            for (int x = 0; x < kTile / 16; ++x) v |= ((m >> (x * 16 / a.P)) & 1u) << x;
+            if (lane == 0) c.valid[(i >> 1) & 3] = v;
+          }
+          // the page the context ends in: its rows past the end hold anything
+          // (NaN too), so that block is copied by hand and filled with zeros
+          const int end = ctx - tile * kTile;
+          const int cut = end < kTile && end % a.P != 0 ? end / a.P : -1;  // warp-uniform
+          if (cut >= 0) {
+            const int id = __shfl_sync(0xffffffffu, page, cut);
+            const unsigned char *src =
+                static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool) +
+                ((size_t)(id < a.num_pages ? id : 0) * a.hkv + h) * a.P * D * 2;
+            const int live = id < a.num_pages ? end % a.P : 0;
+            for (int x = lane; x < a.P * (D / 8); x += 32) {
+              const int r = x / (D / 8), k = x % (D / 8);
+              const uint4 v = r < live ? ldg_nc128(src + ((size_t)r * D + k * 8) * 2)
+                                       : make_uint4(0, 0, 0, 0);
+              sts_u4(dst + sw128(cut * a.P + r, k, kTile), v);
+            }
+            proxy_fence();
+          }
+          __syncwarp();
+          if (lane == 0)
+            bar_arrive_tx(bar, box * (per_tile - (cut >= 0 ? 1 : 0)) * (D / 64));
+          __syncwarp();
+          if (mine && pi != cut)
+            tma_page(is_v ? &a.tmv : &a.tmk, dst + half * (kTile * 128) + pi * box, bar, half * 64, h,
+                     page);
+        }
+        if (!ok) {
+          // stopped early: the copies in flight must land before the CTA ends
+          for (int s = 0; s < L::kSlots; ++s)
+            for (int par = 0; par < 2; ++par) mbar_wait_bounded(smem_u32(&c.full[s]), par, 1000000ull);
+        }
+      }
+    } else if (n > 0) {
+      // ---- quantised pools: codes loaded and converted by three warps
+      constexpr int kRowBytes = KVT == PA_KV_U4_PER_TOKEN ? D / 2 : D;
+      constexpr int kPieces = D / 16;  // 16-code pieces of a row
+      const int lt = tid - kLoadWarp0 * 32;
+      float4 *sz = reinterpret_cast<float4 *>(smem + L::kSzOff);
+      bool ok = true;
+      for (int i = 0; i < 2 * n && ok; ++i) {
+        const int k = i >> 1, tile = t1 - 1 - k;
+        const bool is_v = i & 1;
+        const int slot = i % L::kSlots;
+        if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
+        if (!ok) break;
+        const uint32_t dst = sbase + L::kSlotOff + slot * L::kSlotBytes;
+        const unsigned char *base = static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool);
+        auto row_of = [&](int r) -> long long {  // pool row of key r of the tile, or -1
+          const int tok = tile * kTile + r;
+          if (tok >= ctx) return -1;
+          const int id = __ldg(a.block_tables + (size_t)b * a.max_pages + tok / a.P);
+          if (id < 0 || id >= a.num_pages) return -1;
+          return ((long long)id * a.hkv + h) * a.P + tok % a.P;
+        };
+        if (!is_v) {  // scales and zeros of the tile's keys, and its valid blocks
+          for (int r = lt; r < kTile; r += kLoadThreads) {
+            const long long row = row_of(r);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= 0) {
+              const float2 ks = __ldg(reinterpret_cast<const float2 *>(a.k_sz) + row);
+              const float2 vs = __ldg(reinterpret_cast<const float2 *>(a.v_sz) + row);
+              v = make_float4(ks.x * a.scale_log2, fmaf(ks.x, kCodeShift<KVT>, ks.y) * a.scale_log2,
+                              vs.x, fmaf(vs.x, kCodeShift<KVT>, vs.y));
+            }
+            sz[(k & 3) * kTile + r] = v;
+          }
+          if (lt < 32) {
+            uint32_t v = 0;
+            if (lt < kTile / 16) {
+              const int tok = tile * kTile + lt * 16;
+              const bool bad = tok < ctx && row_of(lt * 16) < 0;
+              if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
+              v = bad ? 0u : 1u;
+            }
+            v = __ballot_sync(0xffffffffu, v != 0);
+            if (lt == 0) c.valid[k & 3] = v;
+          }
+        }
+#pragma unroll 4
+        for (int x = lt; x < kTile * kPieces; x += kLoadThreads) {
+          const int r = x / kPieces, pc = x % kPieces;
+          const long long row = row_of(r);
+          uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          if (row >= 0) {
+            const unsigned char *src = base + row * kRowBytes;
+            if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + pc * 8));
+              const uint32_t ww[2] = {w.x, w.y};
+              codes16<KVT>(ww, out);
+            } else {
+              const uint4 w = ldg_nc128(src + pc * 16);
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              codes16<KVT>(ww, out);
+            }
+          }
+          sts_u4(dst + sw128(r, 2 * pc, kTile), make_uint4(out[0], out[1], out[2], out[3]));
+          sts_u4(dst + sw128(r, 2 * pc + 1, kTile), make_uint4(out[4], out[5], out[6], out[7]));
+        }
+        proxy_fence();
+        bar_arrive(smem_u32(&c.full[slot]));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + sub * kTile + lane_off;
+    const uint32_t t_o = tmem + 2 * kTile + sub * D + lane_off;
+    const uint32_t s_bar = smem_u32(&c.s_full[sub]), p_bar = smem_u32(&c.p_full[sub]);
+    float m_run = -INFINITY, l_run = 0.f, z_run = 0.f;
+    bool ok = true;
+    if (sub < subs && n > 0) {
+      float qsum = 0.f;
+      if constexpr (kQuant && KVT != PA_KV_FP8_PER_TOKEN) {
+        const uint32_t qs = sbase + L::kQOff + sub * L::kQBytes;
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = lds128(qs + sw128(tid & 127, k, kTile));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) qsum += bf16_lo(w[x]) + bf16_hi(w[x]);
+        }
+      }
+      const float slope = a.slopes != nullptr && row_ok
+                              ? __ldg(a.slopes + orow % a.hq) * 1.4426950408889634f
+                              : 0.f;
+      for (int k = 0; k < n; ++k) {
+        ok = ok && wait_bar(s_bar, k & 1, dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int k0 = (t1 - 1 - k) * kTile;
+        float s[kTile];
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 32)
+          tmem_ld32(t_s + c0, reinterpret_cast<uint32_t(&)[32]>(s[c0]));
+        tmem_wait_ld();
+        const float4 *sz = reinterpret_cast<const float4 *>(smem + L::kSzOff) + (k & 3) * kTile;
+        // ---- scores in log2 units
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+          if constexpr (kQuant) {
+            const float4 z = sz[j];
+            s[j] = KVT == PA_KV_FP8_PER_TOKEN ? s[j] * z.x : fmaf(s[j], z.x, z.y * qsum);
+          } else {
+            s[j] *= a.scale_log2;
+          }
+        }
+        if (a.cap_l2 > 0.f) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
+        }
+        if (a.slopes != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) s[j] -= slope * fabsf((float)(pos - k0 - j));
+        }
+        const uint32_t valid = c.valid[k & 3];
+        if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kTile) || valid != 0xFFu) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) {
+            const bool live = k0 + j >= lo && k0 + j < hi && ((valid >> (j / 16)) & 1u);
+            if (!live) s[j] = -INFINITY;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) mx = fmaxf(mx, s[j]);
+        const bool need = mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xffffffffu, need)) {  // tcgen05.ld / st are warp-wide
+          const float m_new = need ? fmaxf(m_run, mx) : m_run;
+          const float alpha = need && m_run != -INFINITY ? fast_exp2(m_run - m_new) : 1.f;
+          m_run = m_new;
+          l_run *= alpha;
+          z_run *= alpha;
+          if (k > 0) {
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t u[32];
+              tmem_ld32(t_o + c0, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * alpha);
+              tmem_st32(t_o + c0, u);
+            }
+          }
+        }
+        const float mref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float p0 = fast_exp2(s[c0 + 2 * j] - mref), p1 = fast_exp2(s[c0 + 2 * j + 1] - mref);
+            l_run += p0 + p1;
+            if constexpr (kQuant) {
+              const float4 z0 = sz[c0 + 2 * j], z1 = sz[c0 + 2 * j + 1];
+              if constexpr (KVT != PA_KV_FP8_PER_TOKEN) z_run += fmaf(p0, z0.w, p1 * z1.w);
+              p0 *= z0.z;
+              p1 *= z1.z;
+            }
+            w[j] = pack_bf16(p0, p1);
+          }
+          tmem_st32(t_s + c0 / 2, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        bar_arrive(p_bar);
+      }
+      if (ok) ok = wait_bar(s_bar, n & 1, dead);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    // ---- the row's result
+    if (sub < subs) {
+      const float inv = l_run > 0.f && ok ? 1.f / l_run : 0.f;
+      const float zero = z_run * inv;
+      const float lse = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t u[32];
+        if (n > 0) {  // CTA-uniform
+          tmem_ld32(t_o + c0, u);
+          tmem_wait_ld();
+        }
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          o[j] = l_run > 0.f ? fmaf(__uint_as_float(u[j]), inv, zero) : 0.f;
+        if (!row_ok) continue;
+        if (a.S > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + (orow * a.S + split) * D + c0);
+          if (l_run > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                pack_bf16(o[8 * j + 4], o[8 * j + 5]),
+                                pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+        }
+      }
+      if (row_ok) {
+        if (a.S > 1) a.lse_part[orow * a.S + split] = lse;
+        else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
+      }
+    }
+    if (!ok) flag_error(a.d_err, PA_DERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    if (*dead && lane == 0) flag_error(a.d_err, PA_DERR_TIMEOUT);
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols));
+  }
+}
+
+// Merge of S partials per (token, query head) row: one warp per row, weights
+// exp(lse_s - max); a partial without weight is not read.
+template <int D>
+__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a) {
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31;
+  const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int first = max(__ldg(a.q_begin), 0), last = min(__ldg(a.q_begin + a.B), a.n);
+  // rows outside the sequences are left as they were
+  if (row >= (size_t)last * a.hq || row < (size_t)first * a.hq) return;
+  const float *lse = a.lse_part + row * a.S;
+  float M = -INFINITY;
+  for (int s = lane; s < a.S; s += 32) M = fmaxf(M, __ldcg(lse + s));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int E = D / 32;
+  float acc[E] = {};
+  float den = 0.f;
+  if (M > -INFINITY) {
+    for (int s = 0; s < a.S; ++s) {
+      const float w = expf(__ldcg(lse + s) - M);
+      if (w == 0.f) continue;
+      den += w;
+      const float *o = a.o_part + (row * a.S + s) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __ldcg(o + e), acc[e]);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (a.lse_out != nullptr && lane == 0) a.lse_out[row] = den > 0.f ? M + logf(den) : -INFINITY;
+}
+
+bool encode_pool(CUtensorMap *map, const void *pool, int D, int P, int hkv, int num_pages) {
+  const TmapEncodeFn f = tmap_encoder();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)hkv, (cuuint64_t)num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)P * D * 2, (cuuint64_t)hkv * P * D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)P, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Once per device and kernel: shared memory opt-in, and a check that the
+// launch brings the registers that the kernel's register split hands out.
+template <int D, int KVT>
+cudaError_t ensure_attr() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, prefill_kernel<D, KVT>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * kThreads < kSoftmaxRegs * 256 + kOtherRegs * 128) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(prefill_kernel<D, KVT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Layout<D, KVT>::kBytes);
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
+template <int D, int KVT>
+cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
+  PrefillArgs a = a_in;
+  cudaError_t e = ensure_attr<D, KVT>();
+  if (e != cudaSuccess) return e;
+  if (KVT == PA_KV_BF16 && (!encode_pool(&a.tmk, a.k_pool, D, a.P, a.hkv, a.num_pages) ||
+                            !encode_pool(&a.tmv, a.v_pool, D, a.P, a.hkv, a.num_pages)))
+    return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)prefill_blocks(a.n, a.B, a.hq / a.hkv) * a.hkv * a.S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D, KVT>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, KVT>, a);
+  if (e != cudaSuccess || a.S == 1) return e;
+  cfg.gridDim = dim3((unsigned)(((long long)a.n * a.hq + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, a);
+}
+
+}  // namespace
+
+// Blocks of 256 rows over all sequences: no more than this, whatever the lengths.
+long long prefill_blocks(int n, int B, int G) { return ((long long)n * G) / kCtaRows + B; }
+
+cudaError_t launch_prefill(int D, int kv_dtype, const PrefillArgs &a, cudaStream_t stream) {
+#define PA_PF(D_, K_) if (D == D_ && kv_dtype == K_) return launch_t<D_, K_>(a, stream)
+  PA_PF(128, PA_KV_BF16); PA_PF(128, PA_KV_U8_PER_TOKEN);
+  PA_PF(128, PA_KV_FP8_PER_TOKEN); PA_PF(128, PA_KV_U4_PER_TOKEN);
+  PA_PF(64, PA_KV_BF16); PA_PF(64, PA_KV_U8_PER_TOKEN);
+  PA_PF(64, PA_KV_FP8_PER_TOKEN); PA_PF(64, PA_KV_U4_PER_TOKEN);
+#undef PA_PF
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

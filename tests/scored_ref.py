@@ -10,11 +10,13 @@ from paged_kv_cache_466_b200 import KVPool, pa_kv_append
 from tests.helpers import DEV
 
 
-def pool_rows(pool, table_row, ctx):
-    """K and V rows of tokens 0 .. ctx - 1, fp64 [ctx, Hkv, D] each."""
+def pool_rows(pool, table_row, ctx, magnitudes=False):
+    """K and V rows of tokens 0 .. ctx - 1, fp64 [ctx, Hkv, D] each; with `magnitudes` also, for
+    K and V, |scale (code - shift)| and |zero + shift scale|, whose sum a quantised row is."""
     P = pool.page_size
     pages = table_row[:-(-ctx // P)].long()
-    out = []
+    shift = {"bf16": 0, "fp8": 0, "u8": 128, "u4": 8}[pool.kind]
+    out, mags = [], []
     for codes, sz in ((pool.k, pool.k_sz), (pool.v, pool.v_sz)):
         x = codes[pages]                                        # [n, Hkv, P, D or D / 2]
         if pool.kind == "u4":
@@ -22,19 +24,26 @@ def pool_rows(pool, table_row, ctx):
         if pool.kind == "fp8":
             x = x.view(torch.float8_e4m3fn)
         x = x.double()
+        m = (x.abs(), torch.zeros_like(x))
         if sz is not None:
-            x = x * sz[pages][..., :1].double() + sz[pages][..., 1:].double()
-        out.append(x.transpose(1, 2).flatten(0, 1)[:ctx])
-    return out
+            s, z = sz[pages][..., :1].double(), sz[pages][..., 1:].double()
+            m = ((s * (x - shift)).abs(), (z + shift * s).abs().expand_as(x))
+            x = x * s + z
+        flat = lambda t: t.transpose(1, 2).flatten(0, 1)[:ctx]
+        out.append(flat(x))
+        mags.append([flat(t) for t in m])
+    return (*out, *mags) if magnitudes else out
 
 
 def attend64(pool, q, q_begin, bt, ctx, scale, softcap=0.0, slopes=None, doc_begin=None,
-             prefix_end=None):
+             prefix_end=None, weighted=False):
     """(out [N, Hq, D], lse [N, Hq], largest |scale| sum |q k| over the visible pairs), fp64; the
-    last tokens of sequence b are its query tokens q_begin[b] .. q_begin[b + 1]."""
+    last tokens of sequence b are its query tokens q_begin[b] .. q_begin[b + 1]. With `weighted`
+    also the softmax-weighted mean of |scale (code - shift)| of the values, [N, Hq, D]."""
     N, Hq, D = q.shape
     G = Hq // pool.num_kv_heads
     out = torch.zeros(N, Hq, D, dtype=torch.float64, device=q.device)
+    mag = torch.zeros_like(out)
     lse = torch.full((N, Hq), -math.inf, dtype=torch.float64, device=q.device)
     s_abs = 0.0
     for b in range(len(ctx)):
@@ -42,7 +51,8 @@ def attend64(pool, q, q_begin, bt, ctx, scale, softcap=0.0, slopes=None, doc_beg
         n = i1 - i0
         if n == 0 or c == 0:
             continue
-        K, V = pool_rows(pool, bt[b], c)
+        K, V, mk, mv = pool_rows(pool, bt[b], c, magnitudes=True)
+        mk = mk[0] + mk[1]
         j = torch.arange(c, device=q.device)
         pos = c - n + torch.arange(n, device=q.device)[:, None]
         see = j <= pos
@@ -54,7 +64,7 @@ def attend64(pool, q, q_begin, bt, ctx, scale, softcap=0.0, slopes=None, doc_beg
             qh = q[i0:i1, h].double()
             x = qh @ K[:, h // G].T * scale
             if see.any():
-                s_abs = max(s_abs, float((qh.abs() @ K[:, h // G].abs().T)[see].max()) * scale)
+                s_abs = max(s_abs, float((qh.abs() @ mk[:, h // G].T)[see].max()) * abs(scale))
             if softcap:
                 x = softcap * torch.tanh(x / softcap)
             if slopes is not None:
@@ -62,8 +72,10 @@ def attend64(pool, q, q_begin, bt, ctx, scale, softcap=0.0, slopes=None, doc_beg
             x = x.masked_fill(~see, -math.inf)
             lse[i0:i1, h] = torch.logsumexp(x, -1)
             p = torch.where(see.any(-1, keepdim=True), torch.softmax(x, -1), torch.zeros_like(x))
-            out[i0:i1, h] = torch.where(p > 0, p, torch.zeros_like(p)) @ V[:, h // G]
-    return out, lse, s_abs
+            p = torch.where(p > 0, p, torch.zeros_like(p))
+            out[i0:i1, h] = p @ V[:, h // G]
+            mag[i0:i1, h] = p @ mv[0][:, h // G]
+    return (out, lse, s_abs, mag) if weighted else (out, lse, s_abs)
 
 
 def make_batch(ctx, Hq, Hkv, D, P, kind, seed=0, slack=3, max_pages=None, amp=1.0):
