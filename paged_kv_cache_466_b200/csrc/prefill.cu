@@ -32,6 +32,8 @@
 // output is; the denominator and all statistics stay fp32.
 #include <atomic>
 #include <cmath>
+#include <cstddef>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -42,18 +44,25 @@ namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;  // raise the running max only past this
+// Of every so many pairs of weights one is exponentiated on the FMA pipe.
+constexpr int kExpEvery = 4;
 constexpr int kTile = 128;            // query rows of a tile, and keys of a tile
 constexpr int kCtaRows = 2 * kTile;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp0 = 9;
-constexpr int kLoadThreads = 96;
 constexpr int kTmemCols = 512;
 // registers per thread after the split of the launch's 168 * 384
 constexpr int kLaunchRegs = 168;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
-static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads, "register split");
+template <int KVT>
+constexpr int kSoftmaxRegs = KVT == PA_KV_BF16 ? 216 : 200;
+template <int KVT>
+constexpr int kOtherRegs = KVT == PA_KV_BF16 ? 72 : 104;
+template <int KVT>
+constexpr bool kSplitFits =
+    kSoftmaxRegs<KVT> * 256 + kOtherRegs<KVT> * 128 <= kLaunchRegs * kThreads;
+static_assert(kSplitFits<PA_KV_BF16> && kSplitFits<PA_KV_U8_PER_TOKEN>, "register split");
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s (a tile takes microseconds)
 
 template <int D, int KVT>
@@ -63,9 +72,10 @@ struct Layout {
   static constexpr int kSlots = KVT == PA_KV_BF16 ? 5 : 4;
   static constexpr int kQOff = 0;
   static constexpr int kSlotOff = 2 * kQBytes;
-  // per key (K scale, K zero, V scale, V zero) of the last four tiles
+  // of the last four tiles: K scale, K zero, V scale, V zero of every key
   static constexpr int kSzOff = kSlotOff + kSlots * kSlotBytes;
-  static constexpr int kSzBytes = KVT == PA_KV_BF16 ? 0 : 4 * kTile * 16;
+  static constexpr int kSzTile = 4 * kTile * 4;
+  static constexpr int kSzBytes = KVT == PA_KV_BF16 ? 0 : 4 * kSzTile;
   static constexpr int kBarOff = kSzOff + kSzBytes;
   static constexpr int kBytes = kBarOff + 512 + 1024;  // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -79,9 +89,11 @@ struct Control {
   uint32_t tmem;
   int32_t dead;                // a bounded wait ran out: everybody stops
   int32_t seq, blk, q0, qlen, ctx;
-  int32_t lo, hi, rows2;       // first / past-the-last key of any row; row tiles in use
-  uint32_t valid[4];           // per tile (mod 4): valid 16-key blocks
+  int32_t lo, hi;              // first / past-the-last key of any row
+  alignas(8) uint8_t valid[4][8];         // per tile (mod 4): 16-key blocks in valid pages
 };
+
+static_assert(offsetof(Control, valid) % 8 == 0 && sizeof(Control) <= 512, "control block");
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -167,32 +179,121 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w) {
   return bf16x2_mul(((w & 0x00800080u) << 8) | ((w & 0x007F007Fu) << 4), 0x7B807B80u);
 }
 
-// 16 codes (8 bytes of INT4, 16 of INT8 / FP8) -> 16 bf16 in element order.
-template <int KVT>
-__device__ __forceinline__ void codes16(const uint32_t *w, uint32_t (&r)[8]) {
-  if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
+// A 16-key block of codes as a warp holds it, 16 bytes per lane and load, and
+// its conversion into a K-major tile. Zero bytes of keys that do not exist
+// become the code shift, whose scale and zero are 0 and whose V weight is 0.
+template <int D, int KVT>
+struct Rows {
+  static constexpr int kRowBytes = KVT == PA_KV_U4_PER_TOKEN ? D / 2 : D;
+  static constexpr int kLoads = 16 * kRowBytes / 512;
+  static __device__ __forceinline__ uint4 convert8(uint32_t w0, uint32_t w1) {  // 8 codes
+    if constexpr (KVT == PA_KV_FP8_PER_TOKEN)
+      return make_uint4(e4m3x2_to_bf16(__byte_perm(w0, 0u, 0x4140)),
+                        e4m3x2_to_bf16(__byte_perm(w0, 0u, 0x4342)),
+                        e4m3x2_to_bf16(__byte_perm(w1, 0u, 0x4140)),
+                        e4m3x2_to_bf16(__byte_perm(w1, 0u, 0x4342)));
+    else
+      return make_uint4(u8x2_to_bf16(__byte_perm(w0, 0u, 0x4140)),
+                        u8x2_to_bf16(__byte_perm(w0, 0u, 0x4342)),
+                        u8x2_to_bf16(__byte_perm(w1, 0u, 0x4140)),
+                        u8x2_to_bf16(__byte_perm(w1, 0u, 0x4342)));
+  }
+  static __device__ __forceinline__ uint4 convert8(uint32_t w) {  // 8 INT4 codes
+    // byte j holds elements 2j (low nibble) and 2j + 1
+    const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __byte_perm(e, o, 0x5140), hi = __byte_perm(e, o, 0x7362);  // in element order
+    return make_uint4(u4x2_to_bf16(__byte_perm(lo, 0u, 0x4140)),
+                      u4x2_to_bf16(__byte_perm(lo, 0u, 0x4342)),
+                      u4x2_to_bf16(__byte_perm(hi, 0u, 0x4140)),
+                      u4x2_to_bf16(__byte_perm(hi, 0u, 0x4342)));
+  }
+  static __device__ __forceinline__ void store(uint32_t tile, int blk, int lane,
+                                               const uint4 (&v)[kLoads]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int k = 0; k < kLoads; ++k) {
+      const int at = (lane + 32 * k) * 16;
+      const int r = blk * 16 + at / kRowBytes;
+      if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
+        const int c0 = at % kRowBytes / 4;  // four 16-byte chunks of bf16
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // byte j: elements 2j (low nibble), 2j + 1
-        const uint32_t b = w[i] >> (8 * j);
-        r[4 * i + j] = u4x2_to_bf16((b & 0xFu) | ((b & 0xF0u) << 12));
+        for (int j = 0; j < 4; ++j) sts_u4(tile + sw128(r, c0 + j, kTile), convert8(w[j]));
+      } else {
+        // lanes of the second 64 columns write their chunks in the other order:
+        // both halves' chunks would share banks
+        const int pc = at % kRowBytes / 16, o = (pc >> 2) & 1;
+        const uint4 a = convert8(v[k].x, v[k].y), b = convert8(v[k].z, v[k].w);
+        sts_u4(tile + sw128(r, 2 * pc + o, kTile), o ? b : a);
+        sts_u4(tile + sw128(r, 2 * pc + 1 - o, kTile), o ? a : b);
       }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = __byte_perm(w[i], 0u, 0x4140), hi = __byte_perm(w[i], 0u, 0x4342);
-      r[2 * i] = KVT == PA_KV_FP8_PER_TOKEN ? e4m3x2_to_bf16(lo) : u8x2_to_bf16(lo);
-      r[2 * i + 1] = KVT == PA_KV_FP8_PER_TOKEN ? e4m3x2_to_bf16(hi) : u8x2_to_bf16(hi);
     }
   }
-}
+};
 template <int KVT>
 constexpr float kCodeShift = KVT == PA_KV_U8_PER_TOKEN ? 128.f : KVT == PA_KV_U4_PER_TOKEN ? 8.f : 0.f;
 
+// ---- two fp32 values per instruction ---------------------------------------------------
+
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
+
+// 2^x for a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f
+// by a polynomial (weighted least squares, 2.8e-06 relative error on
+// [-1/2, 1/2]; exactly 1 at 0, so that everything at and below -127 gives
+// exactly 0) and n added to the exponent. A share of
+// the weights takes this way because the special-function unit, 16 results per
+// clock and SM, would bound the softmax.
+__device__ __forceinline__ f32x2 exp2_fma(f32x2 x) {
+  float x0, x1;
+  unpack2(x, x0, x1);
+  x = pack2(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+  const f32x2 magic = pack2(12582912.f, 12582912.f);  // 1.5 * 2^23
+  const f32x2 t = add2(x, magic);
+  const f32x2 f = add2(x, mul2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f)));
+  f32x2 p = fma2(pack2(0.009582853f, 0.009582853f), f, pack2(0.055906425f, 0.055906425f));
+  p = fma2(p, f, pack2(0.240240986f, 0.240240986f));
+  p = fma2(p, f, pack2(0.693124193f, 0.693124193f));
+  p = fma2(p, f, pack2(1.f, 1.f));
+  float p0, p1, t0, t1;
+  unpack2(p, p0, p1);
+  unpack2(t, t0, t1);
+  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  return pack2(p0, p1);
+}
+
+// How the scores are changed: not at all, capped, or anything (also a scale
+// that is not positive). The first two let the row maximum be taken before
+// the scores are scaled, as both are increasing functions.
+enum { kPlain = 0, kCapped = 1, kGeneral = 2 };
+
 // ---- the kernel ----------------------------------------------------------------------
 
-template <int D, int KVT>
+template <int D, int KVT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a) {
   using L = Layout<D, KVT>;
@@ -262,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.hi = 0;
       c.dead = 0;
       for (int i = 0; i < 5; ++i) {
-        bar_init(smem_u32(&c.full[i]), kQuant ? kLoadThreads : 1);
+        bar_init(smem_u32(&c.full[i]), kQuant ? kTile / 16 : 1);
         bar_init(smem_u32(&c.empty[i]), 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -337,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int32_t *dead = &c.dead;
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<KVT>));
     if (warp == kMmaWarp) {
       if (lane == 0 && n > 0) {
         // ---- MMA issue
@@ -415,13 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!bad) page = id;
             if (bad && mine && half == 0 && !is_v) flag_error(a.d_err, PA_DERR_BAD_PAGE);
           }
-          if (!is_v) {
-            // 16-key blocks of the tile that lie in valid pages
-            const uint32_t m = __ballot_sync(0xffffffffu, !bad && lane < per_tile);
-            uint32_t v = 0;
-            for (int x = 0; x < kTile / 16; ++x) v |= ((m >> (x * 16 / a.P)) & 1u) << x;
-            if (lane == 0) c.valid[(i >> 1) & 3] = v;
-          }
+          if (!is_v && lane < per_tile)
+            for (int x = 0; x < a.P / 16; ++x) c.valid[(i >> 1) & 3][pi * (a.P / 16) + x] = !bad;
           // the page the context ends in: its rows past the end hold anything
           // (NaN too), so that block is copied by hand and filled with zeros
           const int end = ctx - tile * kTile;
@@ -455,77 +551,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (n > 0) {
-      // ---- quantised pools: codes loaded and converted by three warps
-      constexpr int kRowBytes = KVT == PA_KV_U4_PER_TOKEN ? D / 2 : D;
-      constexpr int kPieces = D / 16;  // 16-code pieces of a row
-      const int lt = tid - kLoadWarp0 * 32;
-      float4 *sz = reinterpret_cast<float4 *>(smem + L::kSzOff);
+      // ---- quantised pools: three warps take the tiles' 16-key blocks in
+      // turn. A block's codes (and the scales and zeros of its keys) are loaded
+      // kAhead blocks before they are converted into the slot.
+      using R = Rows<D, KVT>;
+      constexpr int kAhead = 3;
+      const int w = warp - kLoadWarp0;
+      const int total = n * 2 * (kTile / 16);
+      const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
+      auto token_of = [&](int m) { return (t1 - 1 - (m >> 4)) * kTile + (m & 7) * 16; };
+      auto page_of = [&](int m) {  // page of block m; -1: none there, -2: a bad id
+        const int tok = token_of(m);
+        if (m >= total || tok >= ctx) return -1;
+        const int id = __ldg(table + tok / a.P);
+        return id < 0 || id >= a.num_pages ? -2 : id;
+      };
+      struct Block {
+        uint4 v[R::kLoads];
+        float2 sz;
+        int page;
+      };
+      auto fetch = [&](int m, int page) {
+        Block x;
+        x.page = page;
+        const int tok = token_of(m);
+        const int live = page >= 0 ? min(ctx - tok, 16) : 0;
+        const bool is_v = (m >> 3) & 1;
+        const size_t row0 = ((size_t)max(page, 0) * a.hkv + h) * a.P + tok % a.P;
+        const unsigned char *src =
+            static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool) + row0 * R::kRowBytes;
+#pragma unroll
+        for (int k = 0; k < R::kLoads; ++k) {
+          const int at = (lane + 32 * k) * 16;
+          x.v[k] = at / R::kRowBytes < live ? ldg_nc128(src + at) : make_uint4(0, 0, 0, 0);
+        }
+        x.sz = make_float2(0.f, 0.f);
+        if (!is_v && (lane & 15) < live)
+          x.sz = __ldg(reinterpret_cast<const float2 *>(lane < 16 ? a.k_sz : a.v_sz) + row0 + (lane & 15));
+        return x;
+      };
+      Block q[kAhead];
+      int next_page = 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) q[k] = fetch(w + 3 * k, page_of(w + 3 * k));
+      next_page = page_of(w + 3 * kAhead);
       bool ok = true;
-      for (int i = 0; i < 2 * n && ok; ++i) {
-        const int k = i >> 1, tile = t1 - 1 - k;
+      for (int m = w; m < total; m += 3) {
+        const Block x = q[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) q[k] = q[k + 1];
+        q[kAhead - 1] = fetch(m + 3 * kAhead, next_page);
+        next_page = page_of(m + 3 * kAhead + 3);
+        const int i = m >> 3, blk = m & 7, slot = i % L::kSlots;
         const bool is_v = i & 1;
-        const int slot = i % L::kSlots;
         if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = sbase + L::kSlotOff + slot * L::kSlotBytes;
-        const unsigned char *base = static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool);
-        auto row_of = [&](int r) -> long long {  // pool row of key r of the tile, or -1
-          const int tok = tile * kTile + r;
-          if (tok >= ctx) return -1;
-          const int id = __ldg(a.block_tables + (size_t)b * a.max_pages + tok / a.P);
-          if (id < 0 || id >= a.num_pages) return -1;
-          return ((long long)id * a.hkv + h) * a.P + tok % a.P;
-        };
-        if (!is_v) {  // scales and zeros of the tile's keys, and its valid blocks
-          for (int r = lt; r < kTile; r += kLoadThreads) {
-            const long long row = row_of(r);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row >= 0) {
-              const float2 ks = __ldg(reinterpret_cast<const float2 *>(a.k_sz) + row);
-              const float2 vs = __ldg(reinterpret_cast<const float2 *>(a.v_sz) + row);
-              v = make_float4(ks.x * a.scale_log2, fmaf(ks.x, kCodeShift<KVT>, ks.y) * a.scale_log2,
-                              vs.x, fmaf(vs.x, kCodeShift<KVT>, vs.y));
-            }
-            sz[(k & 3) * kTile + r] = v;
-          }
-          if (lt < 32) {
-            uint32_t v = 0;
-            if (lt < kTile / 16) {
-              const int tok = tile * kTile + lt * 16;
-              const bool bad = tok < ctx && row_of(lt * 16) < 0;
-              if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
-              v = bad ? 0u : 1u;
-            }
-            v = __ballot_sync(0xffffffffu, v != 0);
-            if (lt == 0) c.valid[k & 3] = v;
+        if (!is_v) {
+          const int ring = (i >> 1) & 3;
+          float *sz = reinterpret_cast<float *>(smem + L::kSzOff + ring * L::kSzTile) +
+                      (lane < 16 ? 0 : 2 * kTile) + blk * 16 + (lane & 15);
+          const float f = lane < 16 ? a.scale_log2 : 1.f;  // K rows carry the score scale
+          sz[0] = x.sz.x * f;
+          sz[kTile] = fmaf(x.sz.x, kCodeShift<KVT>, x.sz.y) * f;
+          if (lane == 0) {
+            c.valid[ring][blk] = x.page != -2;
+            if (x.page == -2) flag_error(a.d_err, PA_DERR_BAD_PAGE);
           }
         }
-#pragma unroll 4
-        for (int x = lt; x < kTile * kPieces; x += kLoadThreads) {
-          const int r = x / kPieces, pc = x % kPieces;
-          const long long row = row_of(r);
-          uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          if (row >= 0) {
-            const unsigned char *src = base + row * kRowBytes;
-            if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
-              const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + pc * 8));
-              const uint32_t ww[2] = {w.x, w.y};
-              codes16<KVT>(ww, out);
-            } else {
-              const uint4 w = ldg_nc128(src + pc * 16);
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-              codes16<KVT>(ww, out);
-            }
-          }
-          sts_u4(dst + sw128(r, 2 * pc, kTile), make_uint4(out[0], out[1], out[2], out[3]));
-          sts_u4(dst + sw128(r, 2 * pc + 1, kTile), make_uint4(out[4], out[5], out[6], out[7]));
-        }
+        R::store(sbase + L::kSlotOff + slot * L::kSlotBytes, blk, lane, x.v);
         proxy_fence();
-        bar_arrive(smem_u32(&c.full[slot]));
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&c.full[slot]));
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<KVT>));
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + sub * kTile + lane_off;
     const uint32_t t_o = tmem + 2 * kTile + sub * D + lane_off;
@@ -533,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f, z_run = 0.f;
     bool ok = true;
     if (sub < subs && n > 0) {
+      constexpr bool kZero = kQuant && KVT != PA_KV_FP8_PER_TOKEN;  // rows have a zero point
       float qsum = 0.f;
-      if constexpr (kQuant && KVT != PA_KV_FP8_PER_TOKEN) {
+      if constexpr (kZero) {
         const uint32_t qs = sbase + L::kQOff + sub * L::kQBytes;
         for (int k = 0; k < D / 8; ++k) {
           const uint4 v = lds128(qs + sw128(tid & 127, k, kTile));
@@ -543,9 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 4; ++x) qsum += bf16_lo(w[x]) + bf16_hi(w[x]);
         }
       }
-      const float slope = a.slopes != nullptr && row_ok
-                              ? __ldg(a.slopes + orow % a.hq) * 1.4426950408889634f
-                              : 0.f;
+      float slope = 0.f;
+      if constexpr (MODE == kGeneral)
+        if (a.slopes != nullptr && row_ok)
+          slope = __ldg(a.slopes + orow % a.hq) * 1.4426950408889634f;
+      f32x2 l2[2] = {0, 0}, z2 = 0;  // denominator and zero-point sums, by pairs
       for (int k = 0; k < n; ++k) {
         ok = ok && wait_bar(s_bar, k & 1, dead);
         ok = __all_sync(0xffffffffu, ok);
@@ -557,43 +661,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = 0; c0 < kTile; c0 += 32)
           tmem_ld32(t_s + c0, reinterpret_cast<uint32_t(&)[32]>(s[c0]));
         tmem_wait_ld();
-        const float4 *sz = reinterpret_cast<const float4 *>(smem + L::kSzOff) + (k & 3) * kTile;
-        // ---- scores in log2 units
+        const uint32_t sz = sbase + L::kSzOff + (k & 3) * L::kSzTile;
+        if constexpr (kQuant) {  // codes to scores in log2 units
+          const f32x2 qq = pack2(qsum, qsum);
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) {
-          if constexpr (kQuant) {
-            const float4 z = sz[j];
-            s[j] = KVT == PA_KV_FP8_PER_TOKEN ? s[j] * z.x : fmaf(s[j], z.x, z.y * qsum);
-          } else {
-            s[j] *= a.scale_log2;
+          for (int j = 0; j < kTile; j += 4) {
+            const uint4 ks = lds128(sz + j * 4);
+            const float *f = reinterpret_cast<const float *>(&ks);
+            f32x2 u0 = pack2(s[j], s[j + 1]), u1 = pack2(s[j + 2], s[j + 3]);
+            const f32x2 f0 = pack2(f[0], f[1]), f1 = pack2(f[2], f[3]);
+            if constexpr (kZero) {
+              const uint4 kz = lds128(sz + kTile * 4 + j * 4);
+              const float *g = reinterpret_cast<const float *>(&kz);
+              u0 = fma2(u0, f0, mul2(pack2(g[0], g[1]), qq));
+              u1 = fma2(u1, f1, mul2(pack2(g[2], g[3]), qq));
+            } else {
+              u0 = mul2(u0, f0);
+              u1 = mul2(u1, f1);
+            }
+            unpack2(u0, s[j], s[j + 1]);
+            unpack2(u1, s[j + 2], s[j + 3]);
           }
         }
-        if (a.cap_l2 > 0.f) {
+        const uint2 valid = *reinterpret_cast<const uint2 *>(c.valid[k & 3]);
+        const bool all_valid = valid.x == 0x01010101u && valid.y == 0x01010101u;
+        // warp-uniform: every row of the warp sees every key of the tile
+        const bool full = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kTile) && all_valid;
+        float mul = kQuant ? 1.f : a.scale_log2;  // brings s to log2 units
+        bool poly = false;  // capped by the polynomial, in the second pass
+        if constexpr (MODE == kCapped) {
+          float hi4[4], lo4[4];
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
-        }
-        if (a.slopes != nullptr) {
+          for (int i = 0; i < 4; ++i) hi4[i] = lo4[i] = s[i];
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) s[j] -= slope * fabsf((float)(pos - k0 - j));
-        }
-        const uint32_t valid = c.valid[k & 3];
-        if (!__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kTile) || valid != 0xFFu) {
+          for (int j = 0; j < kTile; j += 8)
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) {
-            const bool live = k0 + j >= lo && k0 + j < hi && ((valid >> (j / 16)) & 1u);
-            if (!live) s[j] = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+              hi4[i] = max3(hi4[i], s[j + 2 * i], s[j + 2 * i + 1]);
+              lo4[i] = min3(lo4[i], s[j + 2 * i], s[j + 2 * i + 1]);
+            }
+          const float top = max3(fmaxf(hi4[0], hi4[1]), hi4[2], hi4[3]);
+          const float low = min3(fminf(lo4[0], lo4[1]), lo4[2], lo4[3]);
+          poly = full && __all_sync(0xffffffffu, fmaxf(top, -low) <= a.cap_u);
+          if (!poly) {
+            mul = 1.f;
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.cap_z);
           }
         }
-        float mx = -INFINITY;
+        if constexpr (MODE == kGeneral) {
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) mx = fmaxf(mx, s[j]);
+          for (int j = 0; j < kTile; ++j) s[j] *= mul;
+          mul = 1.f;
+          if (a.cap_l2 > 0.f) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
+          }
+          if (a.slopes != nullptr) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) s[j] -= slope * fabsf((float)(pos - k0 - j));
+          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if ((unsigned)(k0 + j - lo) >= (unsigned)(hi - lo)) s[j] = -INFINITY;
+          if (!all_valid) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j)
+              if (((j < 64 ? valid.x : valid.y) >> (j / 16 % 4 * 8) & 1u) == 0) s[j] = -INFINITY;
+          }
+        }
+        float mx;
+        {
+          float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int j = 0; j < kTile; j += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[j + 2 * i], s[j + 2 * i + 1]);
+          mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+        }
+        if constexpr (MODE == kCapped) {
+          if (poly) {
+            const float y = mx * mx;
+            float r = a.cap_r[5];
+#pragma unroll
+            for (int i = 4; i >= 0; --i) r = fmaf(r, y, a.cap_r[i]);
+            mx *= r;
+          }
+        } else {
+          mx *= mul;
+        }
         const bool need = mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xffffffffu, need)) {  // tcgen05.ld / st are warp-wide
           const float m_new = need ? fmaxf(m_run, mx) : m_run;
           const float alpha = need && m_run != -INFINITY ? fast_exp2(m_run - m_new) : 1.f;
           m_run = m_new;
-          l_run *= alpha;
-          z_run *= alpha;
+          const f32x2 al = pack2(alpha, alpha);
+          l2[0] = mul2(l2[0], al);
+          l2[1] = mul2(l2[1], al);
+          z2 = mul2(z2, al);
           if (k > 0) {
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -606,28 +773,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float mref = m_run == -INFINITY ? 0.f : m_run;
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+        const f32x2 mul_2 = pack2(mul, mul), neg_2 = pack2(neg_m, neg_m);
+        // weights: P over the scores' own columns, two keys per column
+        auto weights = [&](auto poly_c) {
 #pragma unroll
-        for (int c0 = 0; c0 < kTile; c0 += 64) {
-          uint32_t w[32];
+          for (int c0 = 0; c0 < kTile; c0 += 64) {
+            uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float p0 = fast_exp2(s[c0 + 2 * j] - mref), p1 = fast_exp2(s[c0 + 2 * j + 1] - mref);
-            l_run += p0 + p1;
-            if constexpr (kQuant) {
-              const float4 z0 = sz[c0 + 2 * j], z1 = sz[c0 + 2 * j + 1];
-              if constexpr (KVT != PA_KV_FP8_PER_TOKEN) z_run += fmaf(p0, z0.w, p1 * z1.w);
-              p0 *= z0.z;
-              p1 *= z1.z;
+            for (int j = 0; j < 32; j += 2) {
+              f32x2 p[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const f32x2 u = pack2(s[c0 + 2 * (j + i)], s[c0 + 2 * (j + i) + 1]);
+                f32x2 x;
+                if constexpr (decltype(poly_c)::value) {
+                  const f32x2 y = mul2(u, u);
+                  f32x2 r = pack2(a.cap_r[5], a.cap_r[5]);
+#pragma unroll
+                  for (int e = 4; e >= 0; --e) r = fma2(r, y, pack2(a.cap_r[e], a.cap_r[e]));
+                  x = fma2(u, r, neg_2);
+                } else {
+                  x = fma2(u, mul_2, neg_2);
+                }
+                if (!decltype(poly_c)::value && (j + i) % kExpEvery == kExpEvery - 1) {
+                  p[i] = exp2_fma(x);
+                } else {
+                  float x0, x1;
+                  unpack2(x, x0, x1);
+                  p[i] = pack2(fast_exp2(x0), fast_exp2(x1));
+                }
+                l2[i] = add2(l2[i], p[i]);
+              }
+              if constexpr (kQuant) {
+                const uint4 vs = lds128(sz + 2 * kTile * 4 + (c0 + 2 * j) * 4);
+                const float *f = reinterpret_cast<const float *>(&vs);
+                if constexpr (kZero) {
+                  const uint4 vz = lds128(sz + 3 * kTile * 4 + (c0 + 2 * j) * 4);
+                  const float *g = reinterpret_cast<const float *>(&vz);
+                  z2 = fma2(p[0], pack2(g[0], g[1]), z2);
+                  z2 = fma2(p[1], pack2(g[2], g[3]), z2);
+                }
+                p[0] = mul2(p[0], pack2(f[0], f[1]));
+                p[1] = mul2(p[1], pack2(f[2], f[3]));
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float p0, p1;
+                unpack2(p[i], p0, p1);
+                w[j + i] = pack_bf16(p0, p1);
+              }
             }
-            w[j] = pack_bf16(p0, p1);
+            tmem_st32(t_s + c0 / 2, w);
           }
-          tmem_st32(t_s + c0 / 2, w);
+        };
+        if constexpr (MODE == kCapped) {
+          if (poly) weights(std::true_type{});
+          else weights(std::false_type{});
+        } else {
+          weights(std::false_type{});
         }
         tmem_wait_st();
         tc_fence_before();
         bar_arrive(p_bar);
       }
+      float x0, x1;
+      unpack2(add2(l2[0], l2[1]), x0, x1);
+      l_run = x0 + x1;
+      unpack2(z2, x0, x1);
+      z_run = x0 + x1;
       if (ok) ok = wait_bar(s_bar, n & 1, dead);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
@@ -731,7 +945,7 @@ bool encode_pool(CUtensorMap *map, const void *pool, int D, int P, int hkv, int 
 
 // Once per device and kernel: shared memory opt-in, and a check that the
 // launch brings the registers that the kernel's register split hands out.
-template <int D, int KVT>
+template <int D, int KVT, int MODE>
 cudaError_t ensure_attr() {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -740,19 +954,19 @@ cudaError_t ensure_attr() {
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_kernel<D, KVT>);
+  e = cudaFuncGetAttributes(&fa, prefill_kernel<D, KVT, MODE>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs * kThreads < kSoftmaxRegs * 256 + kOtherRegs * 128) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(prefill_kernel<D, KVT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (fa.numRegs * kThreads < kSoftmaxRegs<KVT> * 256 + kOtherRegs<KVT> * 128) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(prefill_kernel<D, KVT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Layout<D, KVT>::kBytes);
   if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
   return e;
 }
 
-template <int D, int KVT>
-cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
+template <int D, int KVT, int MODE>
+cudaError_t launch_mode(const PrefillArgs &a_in, cudaStream_t stream) {
   PrefillArgs a = a_in;
-  cudaError_t e = ensure_attr<D, KVT>();
+  cudaError_t e = ensure_attr<D, KVT, MODE>();
   if (e != cudaSuccess) return e;
   if (KVT == PA_KV_BF16 && (!encode_pool(&a.tmk, a.k_pool, D, a.P, a.hkv, a.num_pages) ||
                             !encode_pool(&a.tmv, a.v_pool, D, a.P, a.hkv, a.num_pages)))
@@ -767,12 +981,31 @@ cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, KVT>, a);
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel<D, KVT, MODE>, a);
   if (e != cudaSuccess || a.S == 1) return e;
   cfg.gridDim = dim3((unsigned)(((long long)a.n * a.hq + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, a);
+}
+
+template <int D, int KVT>
+cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
+  PrefillArgs a = a_in;
+  if (a.slopes != nullptr || !(a.scale_log2 > 0.f)) return launch_mode<D, KVT, kGeneral>(a, stream);
+  if (!(a.cap_l2 > 0.f)) return launch_mode<D, KVT, kPlain>(a, stream);
+  // cap tanh(z), z = cap_z u, as u R(u^2) with the polynomial of tanh_f32;
+  // u is q.k (bf16 pools) or the score in log2 units
+  const double z = KVT == PA_KV_BF16 ? (double)a.scale_log2 * a.inv_cap : (double)a.inv_cap;
+  const double c[6] = {1.0, -0.33333282, 0.13331442, -0.05373971, 0.02063908, -0.00570498};
+  double zz = z;
+  for (int i = 0; i < 6; ++i, zz *= z * z) a.cap_r[i] = (float)(a.cap_l2 * c[i] * zz);
+  a.cap_z = (float)z;
+  a.cap_u = (float)(0.625 / z);
+  // coefficients that fp32 cannot hold (a tiny cap or scale) leave the other way
+  for (int i = 0; i < 6; ++i)
+    if (!std::isfinite(a.cap_r[i]) || !std::isfinite(a.cap_u)) return launch_mode<D, KVT, kGeneral>(a, stream);
+  return launch_mode<D, KVT, kCapped>(a, stream);
 }
 
 }  // namespace
