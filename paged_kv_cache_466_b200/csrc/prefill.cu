@@ -13,8 +13,9 @@
 //   warps 0-3, 4-7   softmax of row tile 0, 1: thread = row = TMEM lane
 //   warp 8           issues the MMAs (one thread)
 //   warps 9-11       bring K and V tiles into shared memory: bf16 pools by TMA
-//                    (one box per page and 64 columns), quantised pools by
-//                    loads and exact conversion of the codes to bf16
+//                    (one box per page and 64 columns; warp 9 K, warp 10 V),
+//                    quantised pools by loads and exact conversion of the
+//                    codes to bf16
 //
 //   S[128 x 128] = Q K^T  : Q and K K-major, 128-byte-swizzled in shared memory
 //   O[128 x D]  += P V    : P from tensor memory (bf16, over the scores' own
@@ -128,6 +129,16 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_arrive_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
+}
+// One lane of a converged warp, the same every time. The MMA and copy loops run
+// warp-uniformly and only the issue itself is elected: their operands then
+// stay in uniform registers (in a branch of one lane every operand of every
+// MMA is moved there again, 97 clocks an MMA instead of 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void proxy_fence() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -440,109 +451,127 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<KVT>));
     if (warp == kMmaWarp) {
-      if (lane == 0 && n > 0) {
+      if (n > 0) {
         // ---- MMA issue
-        auto slot_addr = [&](int i) { return sbase + L::kSlotOff + (i % L::kSlots) * L::kSlotBytes; };
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         auto wait_slot = [&](int i) {
-          return wait_bar(smem_u32(&c.full[i % L::kSlots]), (i / L::kSlots) & 1, dead);
+          const bool done =
+              wait_bar(smem_u32(&c.full[i % L::kSlots]), (i / L::kSlots) & 1, dead);
+          return (bool)__all_sync(0xffffffffu, done);
         };
+        // operands advance by constants inside a tile: one addition per MMA
+        const uint64_t q_desc = smem_desc(sbase + L::kQOff, 16, 1024);
+        const uint64_t k_desc = smem_desc(sbase + L::kSlotOff, 16, 1024);
+        const uint64_t v_desc = smem_desc(sbase + L::kSlotOff, kTile * 128, 1024);
         auto issue_s = [&](int sb, int k) {
-          const uint32_t q0 = sbase + L::kQOff + sb * L::kQBytes;
-          const uint32_t k0 = slot_addr(2 * k);
+          const uint64_t q0 = q_desc + sb * (L::kQBytes >> 4);
+          const uint64_t k0 = k_desc + (2 * k) % L::kSlots * (L::kSlotBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-            umma_bf16(tmem + sb * kTile, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024),
-                      instr_desc(kTile, false), kk > 0);
+            const uint32_t off = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+            umma_bf16(tm + sb * kTile, q0 + off, k0 + off, instr_desc(kTile, false), kk > 0);
           }
         };
         auto issue_pv = [&](int sb, int k) {
-          const uint32_t v0 = slot_addr(2 * k + 1);
+          const uint64_t v0 = v_desc + (2 * k + 1) % L::kSlots * (L::kSlotBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16_ts(tmem + 2 * kTile + sb * D, tmem + sb * kTile + kk * 8,
-                         smem_desc(v0 + kk * 2048, kTile * 128, 1024), instr_desc(D, true),
-                         k > 0 || kk > 0);
+            umma_bf16_ts(tm + 2 * kTile + sb * D, tm + sb * kTile + kk * 8,
+                         v0 + ((kk * 2048) >> 4), instr_desc(D, true), k > 0 || kk > 0);
         };
         bool ok = wait_slot(0);
         tc_fence_after();
-        for (int sb = 0; ok && sb < subs; ++sb) {
-          issue_s(sb, 0);
-          umma_commit(smem_u32(&c.s_full[sb]));
+        if (ok && elect_one()) {
+          for (int sb = 0; sb < subs; ++sb) {
+            issue_s(sb, 0);
+            umma_commit(smem_u32(&c.s_full[sb]));
+          }
+          umma_commit(smem_u32(&c.empty[0]));
         }
-        if (ok) umma_commit(smem_u32(&c.empty[0]));
+        __syncwarp();
         for (int k = 0; ok && k < n; ++k) {
           ok = wait_slot(2 * k + 1);
           if (ok && k + 1 < n) ok = wait_slot(2 * k + 2);
           for (int sb = 0; ok && sb < subs; ++sb) {
-            ok = wait_bar(smem_u32(&c.p_full[sb]), k & 1, dead);
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&c.p_full[sb]), k & 1, dead));
             if (!ok) break;
             tc_fence_after();
-            issue_pv(sb, k);
-            if (k + 1 < n) issue_s(sb, k + 1);
-            umma_commit(smem_u32(&c.s_full[sb]));
+            if (elect_one()) {
+              issue_pv(sb, k);
+              if (k + 1 < n) issue_s(sb, k + 1);
+              umma_commit(smem_u32(&c.s_full[sb]));
+            }
+            __syncwarp();
           }
-          if (ok) {
+          if (ok && elect_one()) {
             umma_commit(smem_u32(&c.empty[(2 * k + 1) % L::kSlots]));
             if (k + 1 < n) umma_commit(smem_u32(&c.empty[(2 * k + 2) % L::kSlots]));
           }
+          __syncwarp();
         }
       }
-      __syncwarp();
     } else if constexpr (!kQuant) {
-      // ---- K and V tiles by TMA, one warp: lane = (page of the tile, 64 columns)
-      if (warp == kLoadWarp0 && n > 0) {
+      // ---- K tiles (warp 9) and V tiles (warp 10) by TMA, page by page
+      if (warp < kLoadWarp0 + 2 && n > 0) {
+        const bool is_v = warp != kLoadWarp0;
+        const CUtensorMap *map = is_v ? &a.tmv : &a.tmk;
         const int per_tile = kTile / a.P;
-        const int pi = lane % per_tile, half = lane / per_tile;
-        const bool mine = half < D / 64;
         const uint32_t box = (uint32_t)a.P * 128;
+        const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
+        // lane x: the id of page x of tile k; past the context -1
+        auto page_of = [&](int k) {
+          const int tok = (t1 - 1 - k) * kTile + lane * a.P;
+          return k < n && lane < per_tile && tok < ctx ? __ldg(table + tok / a.P) : -1;
+        };
+        int id = page_of(0);
         bool ok = true;
-        for (int i = 0; i < 2 * n && ok; ++i) {
-          const int tile = t1 - 1 - (i >> 1);
-          const bool is_v = i & 1;
-          const int slot = i % L::kSlots;
+        for (int k = 0; k < n; ++k) {
+          const int tile = t1 - 1 - k;
+          const int next = page_of(k + 1);
+          const bool past = tile * kTile + lane * a.P >= ctx;
+          const bool bad = lane < per_tile && !past && (id < 0 || id >= a.num_pages);
+          const int page = past || bad ? a.num_pages : id;  // past the pool: zeros
+          if (!is_v && lane < per_tile) {
+            if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
+            for (int x = 0; x < a.P / 16; ++x) c.valid[k & 3][lane * (a.P / 16) + x] = !bad;
+          }
+          const int i = 2 * k + is_v, slot = i % L::kSlots;
           if (i >= L::kSlots)
             ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t dst = sbase + L::kSlotOff + slot * L::kSlotBytes;
           const uint32_t bar = smem_u32(&c.full[slot]);
-          const int tok0 = tile * kTile + pi * a.P;
-          int page = a.num_pages;  // past the pool: zeros
-          bool bad = false;
-          if (tok0 < ctx) {
-            const int id = __ldg(a.block_tables + (size_t)b * a.max_pages + tok0 / a.P);
-            bad = id < 0 || id >= a.num_pages;
-            if (!bad) page = id;
-            if (bad && mine && half == 0 && !is_v) flag_error(a.d_err, PA_DERR_BAD_PAGE);
-          }
-          if (!is_v && lane < per_tile)
-            for (int x = 0; x < a.P / 16; ++x) c.valid[(i >> 1) & 3][pi * (a.P / 16) + x] = !bad;
           // the page the context ends in: its rows past the end hold anything
           // (NaN too), so that block is copied by hand and filled with zeros
           const int end = ctx - tile * kTile;
           const int cut = end < kTile && end % a.P != 0 ? end / a.P : -1;  // warp-uniform
           if (cut >= 0) {
-            const int id = __shfl_sync(0xffffffffu, page, cut);
+            const int pg = __shfl_sync(0xffffffffu, page, cut);
             const unsigned char *src =
                 static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool) +
-                ((size_t)(id < a.num_pages ? id : 0) * a.hkv + h) * a.P * D * 2;
-            const int live = id < a.num_pages ? end % a.P : 0;
+                ((size_t)(pg < a.num_pages ? pg : 0) * a.hkv + h) * a.P * D * 2;
+            const int live = pg < a.num_pages ? end % a.P : 0;
             for (int x = lane; x < a.P * (D / 8); x += 32) {
-              const int r = x / (D / 8), k = x % (D / 8);
-              const uint4 v = r < live ? ldg_nc128(src + ((size_t)r * D + k * 8) * 2)
+              const int r = x / (D / 8), j = x % (D / 8);
+              const uint4 v = r < live ? ldg_nc128(src + ((size_t)r * D + j * 8) * 2)
                                        : make_uint4(0, 0, 0, 0);
-              sts_u4(dst + sw128(cut * a.P + r, k, kTile), v);
+              sts_u4(dst + sw128(cut * a.P + r, j, kTile), v);
             }
             proxy_fence();
           }
           __syncwarp();
-          if (lane == 0)
-            bar_arrive_tx(bar, box * (per_tile - (cut >= 0 ? 1 : 0)) * (D / 64));
-          __syncwarp();
-          if (mine && pi != cut)
-            tma_page(is_v ? &a.tmv : &a.tmk, dst + half * (kTile * 128) + pi * box, bar, half * 64, h,
-                     page);
+          if (elect_one()) bar_arrive_tx(bar, box * (per_tile - (cut >= 0 ? 1 : 0)) * (D / 64));
+          for (int x = 0; x < per_tile; ++x) {
+            const int pg = __shfl_sync(0xffffffffu, page, x);
+            if (x != cut && elect_one()) {
+#pragma unroll
+              for (int half = 0; half < D / 64; ++half)
+                tma_page(map, dst + half * (kTile * 128) + x * box, bar, half * 64, h, pg);
+            }
+            __syncwarp();
+          }
+          id = next;
         }
         if (!ok) {
           // stopped early: the copies in flight must land before the CTA ends
