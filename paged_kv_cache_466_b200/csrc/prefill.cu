@@ -619,23 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.sz = __ldg(reinterpret_cast<const float2 *>(lane < 16 ? a.k_sz : a.v_sz) + row0 + (lane & 15));
         return x;
       };
-      Block q[kAhead];
-      int next_page = 0;
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) q[k] = fetch(w + 3 * k, page_of(w + 3 * k));
-      next_page = page_of(w + 3 * kAhead);
-      bool ok = true;
-      for (int m = w; m < total; m += 3) {
-        const Block x = q[0];
-#pragma unroll
-        for (int k = 0; k + 1 < kAhead; ++k) q[k] = q[k + 1];
-        q[kAhead - 1] = fetch(m + 3 * kAhead, next_page);
-        next_page = page_of(m + 3 * kAhead + 3);
+      // writes block m into its slot; false when the wait for the slot ran out
+      auto put = [&](int m, const Block &x) {
         const int i = m >> 3, blk = m & 7, slot = i % L::kSlots;
         const bool is_v = i & 1;
+        bool ok = true;
         if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) return false;
         if (!is_v) {
           const int ring = (i >> 1) & 3;
           float *sz = reinterpret_cast<float *>(smem + L::kSzOff + ring * L::kSzTile) +
@@ -652,6 +642,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&c.full[slot]));
+        return true;
+      };
+      // the buffers keep their registers (moving one that a load still fills
+      // would wait for the load), so the loop is unrolled over them
+      Block q[kAhead];
+      int page[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        q[k] = fetch(w + 3 * k, page_of(w + 3 * k));
+        page[k] = page_of(w + 3 * (kAhead + k));
+      }
+      for (int m0 = w; m0 < total; m0 += 3 * kAhead) {
+        bool stop = false;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int m = m0 + 3 * k;
+          if (m < total && !stop) {
+            stop = !put(m, q[k]);
+            q[k] = fetch(m + 3 * kAhead, page[k]);
+            page[k] = page_of(m + 6 * kAhead);
+          }
+        }
+        if (stop) break;
       }
     }
   } else {
