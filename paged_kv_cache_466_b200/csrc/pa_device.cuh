@@ -35,6 +35,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src,
       : "memory");
 }
 
+// The same for 8 bytes (0 or 8 read).
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::: "memory");
 }

@@ -196,7 +196,7 @@ struct PrefillArgs {
   float scale_log2;
   float cap_l2;   // softcap * log2(e); 0: not capped
   float inv_cap;  // 1 / cap_l2
-  float cap_r[6]; // capped scores as u R(u^2) for |u| <= cap_u; set by the launch
+  float cap_r[4]; // capped scores as u R(u^2) for |u| <= cap_u; set by the launch
   float cap_u;
   float cap_z;
   const float *slopes;
