@@ -47,7 +47,7 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;   // raise the running max only past this
 constexpr float kQuickMost = 1048576.f;  // largest weight sum of a tile done without a maximum
 // Of every so many pairs of weights one is exponentiated on the FMA pipe.
-constexpr int kExpEvery = 4, kExpEveryCapped = 1024;
+constexpr int kExpEvery = 1024, kExpEveryCapped = 1024;
 constexpr int kTile = 128;            // query rows of a tile (the MMA's M)
 constexpr int kKeys = 128;            // keys of a tile
 constexpr int kCtaRows = 2 * kTile;
@@ -65,9 +65,9 @@ constexpr int kLoaders = kThreads<KVT> / 32 - kLoadWarp0;  // warps (bf16 pools 
 template <int KVT>
 constexpr int kLaunchRegs = KVT == PA_KV_BF16 ? 168 : 128;
 template <int KVT>
-constexpr int kSoftmaxRegs = KVT == PA_KV_BF16 ? 216 : 208;
+constexpr int kSoftmaxRegs = KVT == PA_KV_BF16 ? 224 : 208;
 template <int KVT>
-constexpr int kOtherRegs = KVT == PA_KV_BF16 ? 72 : 48;
+constexpr int kOtherRegs = KVT == PA_KV_BF16 ? 56 : 48;
 template <int KVT>
 constexpr int kSplitRegs = kSoftmaxRegs<KVT> * kSoftmaxThreads +
                            kOtherRegs<KVT> * (kThreads<KVT> - kSoftmaxThreads);
@@ -103,6 +103,7 @@ struct Layout {
 // Shared control block behind the tiles.
 struct Control {
   uint64_t full[5], empty[5];    // K / V slots
+  uint64_t q_full;               // queries in shared memory
   uint64_t s_full[2];            // scores of a row tile (and the PV before them) done
   uint64_t p_full[2];            // P of a row tile stored, O rescaled
   uint32_t tmem;
@@ -350,68 +351,65 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
   const int flat = blockIdx.x / a.hkv / a.S;
   const int G = a.hq / a.hkv;
 
-  // ---- which sequence and rows: warp 0 adds up the sequences' blocks. Blocks
-  // are taken from the last to the first, so that with causal masks the ones
-  // with most keys start first.
+  // ---- which sequence and rows: warp 0 adds up the sequences' blocks, 32
+  // sequences at a time (their lengths stay in registers when that is all).
+  // Blocks are taken from the last to the first, so that with causal masks the
+  // ones with most keys start first.
   if (warp == 0) {
-    auto blocks_of = [&](int b, int &s, int &len) {
+    int s = 0, len = 0, ctx = 0, nb = 0;
+    auto load = [&](int b) {
+      s = len = ctx = nb = 0;
+      if (b >= a.B) return;
       const int q0 = __ldg(a.q_begin + b), q1 = __ldg(a.q_begin + b + 1);
+      ctx = __ldg(a.ctx + b);
       s = max(q0, 0);
       len = max(min(q1, a.n) - s, 0);
       if (blockIdx.x == 0 && (q0 < 0 || q1 > a.n || q1 < q0)) flag_error(a.d_err, PA_DERR_BAD_SEQ);
-      return (int)(((long long)len * G + kCtaRows - 1) / kCtaRows);
+      nb = (int)(((long long)len * G + kCtaRows - 1) / kCtaRows);
     };
+    if (lane == 0) c.seq = -1;
     int total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int s, len;
-      const int nb = b0 + lane < a.B ? blocks_of(b0 + lane, s, len) : 0;
+      load(b0 + lane);
       total += __reduce_add_sync(0xffffffffu, nb);
     }
-    if (lane == 0) c.seq = -1;
-    __syncwarp();
     const int want = total - 1 - flat;
-    if (want >= 0) {
-      int before = 0;
-      for (int b0 = 0; b0 < a.B; b0 += 32) {
-        int s = 0, len = 0;
-        const int nb = b0 + lane < a.B ? blocks_of(b0 + lane, s, len) : 0;
-        int incl = nb;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B && want >= before; b0 += 32) {  // (want < 0: past the last block)
+      if (a.B > 32) load(b0 + lane);
+      int incl = nb;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (want >= before + incl - nb && want < before + incl) {
+        c.seq = b0 + lane;
+        c.blk = want - (before + incl - nb);
+        c.q0 = s;
+        c.qlen = len;
+        if (ctx < len || ctx > a.max_pages * a.P) {  // no such context: sees nothing
+          flag_error(a.d_err, PA_DERR_BAD_CTX);
+          ctx = 0;
         }
-        if (want >= before + incl - nb && want < before + incl) {
-          const int b = b0 + lane;
-          c.seq = b;
-          c.blk = want - (before + incl - nb);
-          c.q0 = s;
-          c.qlen = len;
-          int ctx = __ldg(a.ctx + b);
-          if (ctx < len || ctx > a.max_pages * a.P) {  // no such context: sees nothing
-            flag_error(a.d_err, PA_DERR_BAD_CTX);
-            ctx = 0;
-          }
-          c.ctx = ctx;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-        if (want < before) break;
+        c.ctx = ctx;
       }
+      before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      c.lo = 0x7fffffff;
-      c.hi = 0;
-      c.dead = 0;
-      for (int i = 0; i < L::kSlots; ++i) {
-        bar_init(smem_u32(&c.full[i]), kQuant ? kKeys / 16 : 1);
-        bar_init(smem_u32(&c.empty[i]), 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        bar_init(smem_u32(&c.s_full[i]), 1);
-        bar_init(smem_u32(&c.p_full[i]), kTile);
-      }
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (tid == 32) {
+    c.lo = 0x7fffffff;
+    c.hi = 0;
+    c.dead = 0;
+    for (int i = 0; i < L::kSlots; ++i) {
+      bar_init(smem_u32(&c.full[i]), kQuant ? kKeys / 16 : 1);
+      bar_init(smem_u32(&c.empty[i]), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(smem_u32(&c.s_full[i]), 1);
+      bar_init(smem_u32(&c.p_full[i]), kTile);
+    }
+    bar_init(smem_u32(&c.q_full), kSoftmaxThreads);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   if (c.seq < 0) return;  // CTA-uniform: past the last block
@@ -437,16 +435,20 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       if (a.doc_begin != nullptr) lo = max(__ldg(a.doc_begin + c.q0 + tok), 0);
       if (hi <= lo) lo = hi = 0;
     }
-    const unsigned char *src = static_cast<const unsigned char *>(a.q) + orow * D * 2;
+    // the warp's 32 query rows, D / 8 lanes a row (rows past the last: zeros)
     const uint32_t dst = sbase + L::kQOff + sub * L::kQBytes;
+    constexpr int kRowLanes = D / 8;
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) {
-      if constexpr (kQuant) {
-        const uint4 v = row_ok ? ldg_nc128(src + k * 16) : make_uint4(0, 0, 0, 0);
-        sts_u4(dst + sw128(rl, k, kTile), place8<KVT>(v));
-      } else {
-        cp_async16(dst + sw128(rl, k, kTile), src + k * 16, row_ok ? 16u : 0u);
-      }
+    for (int i = 0; i < kRowLanes; ++i) {
+      const int r = i * (32 / kRowLanes) + lane / kRowLanes, k = lane % kRowLanes;
+      const size_t from = __shfl_sync(0xffffffffu, (unsigned long long)orow, r);
+      const bool live = __shfl_sync(0xffffffffu, (int)row_ok, r) != 0;
+      const unsigned char *src = static_cast<const unsigned char *>(a.q) + from * D * 2 + k * 16;
+      const uint32_t to = dst + sw128((warp & 3) * 32 + r, k, kTile);
+      if constexpr (kQuant)
+        sts_u4(to, place8<KVT>(live ? ldg_nc128(src) : make_uint4(0, 0, 0, 0)));
+      else
+        cp_async16(to, src, live ? 16u : 0u);
     }
     cp_async_commit();
     const bool sees = row_ok && hi > lo;
@@ -463,10 +465,8 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  cp_async_wait<0>();
-  proxy_fence();
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // the key range and the TMEM address; the queries are still on their way
   tc_fence_after();
 
   // ---- this split's key tiles [t0, t1), walked from t1 - 1 down
@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
             umma_bf16_ts(tm + 2 * kKeys + sb * D, tm + sb * kKeys + kk * 8, v0 + ((kk * 2048) >> 4),
                          instr_desc(D, true), k > 0 || kk > 0);
         };
-        bool ok = wait_slot(0);
+        bool ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&c.q_full), 0, dead));
+        ok = ok && wait_slot(0);
         tc_fence_after();
         if (ok && elect_one()) {
           for (int sb = 0; sb < subs; ++sb) {
@@ -705,6 +706,9 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<KVT>));
+    cp_async_wait<0>();
+    proxy_fence();
+    bar_arrive(smem_u32(&c.q_full));
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + sub * kKeys + lane_off;
     const uint32_t t_o = tmem + 2 * kKeys + sub * D + lane_off;
@@ -714,6 +718,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       constexpr bool kZero = kQuant && KVT != PA_KV_FP8_PER_TOKEN;  // rows have a zero point
       float qsum = 0.f;
       if constexpr (kZero) {
+        __syncwarp();  // a warp's rows are loaded by the warp
         const uint32_t qs = sbase + L::kQOff + sub * L::kQBytes;
         for (int k = 0; k < D / 8; ++k) {
           const uint4 v = lds128(qs + sw128(rl, k, kTile));
@@ -842,19 +847,19 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         // kQuickMost (weights above 1 are carried as exactly as those below) and, capped, all
         // scores lie where the polynomial is good. Else the tile is done
         // again, below, from the scores still in registers.
-        bool done = false;
+        bool quick = MODE != kGeneral && full && __all_sync(0xffffffffu, m_run > -INFINITY);
         if constexpr (MODE != kGeneral) {
-          if (full && __all_sync(0xffffffffu, m_run > -INFINITY)) {
-            bool good;
+          if (quick) {
+            bool good = true;
             if constexpr (MODE == kCapped)
               good = weights(std::true_type{}, mul, m_run) <= a.cap_u * a.cap_u;
             else
-              good = (weights(std::false_type{}, mul, m_run), true);
-            done = __all_sync(0xffffffffu, good && lt < kQuickMost);
+              weights(std::false_type{}, mul, m_run);
+            quick = __all_sync(0xffffffffu, good && lt < kQuickMost);
+            if (!quick) tmem_wait_st();  // this P is written over
           }
         }
-        if (!done) {
-          tmem_wait_st();  // the quick way's P is written over
+        if (!quick) {
           if constexpr (MODE == kCapped) {
             mul = 1.f;
 #pragma unroll
@@ -897,7 +902,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
             l_run *= alpha;
             z_run *= alpha;
             if (k > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int c0 = 0; c0 < D; c0 += 16) {
                 uint32_t u[16];
                 tmem_ld16(t_o + c0, u);
@@ -926,35 +931,62 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       const float inv = none ? 0.f : 1.f / l_run;
       const float zero = z_run * inv;
       const float lse = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+      // The row tile's queries are not needed any more: the warp's rows go
+      // through their place in shared memory, 256 bytes (16 pieces, swizzled by
+      // row) a row and turn, and out in whole lines.
+      const uint32_t stage = sbase + L::kQOff + sub * L::kQBytes + (warp & 3) * (L::kQBytes / 4);
+      constexpr int kRowPieces = D / 8;  // of bf16; a turn of fp32 partials holds D / 2 columns
+      auto out_rows = [&](auto part_c, int c0) {
+        constexpr bool kPart = decltype(part_c)::value;
+        constexpr int kCols = kPart ? D / 2 : D;
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t u[32];
-        if (n > 0) {  // CTA-uniform
-          tmem_ld32(t_o + c0, u);
-          tmem_wait_ld();
-        }
-        float o[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float v = __uint_as_float(u[(j & ~7) + place_of<KVT>(j & 7)]);
-          o[j] = none ? 0.f : fmaf(v, inv, zero);
-        }
-        if (!row_ok) continue;
-        if (a.S > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(a.o_part + (orow * a.S + split) * D + c0);
-          if (!none) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (int x = 0; x < kCols; x += 32) {
+          uint32_t u[32];
+          if (n > 0) {  // CTA-uniform
+            tmem_ld32(t_o + c0 + x, u);
+            tmem_wait_ld();
           }
-        } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
+          float o[32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
-                                pack_bf16(o[8 * j + 4], o[8 * j + 5]),
-                                pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+          for (int j = 0; j < 32; ++j) {
+            const float v = __uint_as_float(u[(j & ~7) + place_of<KVT>(j & 7)]);
+            o[j] = none ? 0.f : fmaf(v, inv, zero);
+          }
+          constexpr int kEach = kPart ? 4 : 8;  // columns per piece
+#pragma unroll
+          for (int j = 0; j < 32 / kEach; ++j) {
+            const int pc = x / kEach + j;
+            const uint32_t to = stage + lane * kRowPieces * 16 + ((pc ^ (lane & (kRowPieces - 1))) << 4);
+            if constexpr (kPart)
+              sts_u4(to, make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                                    __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3])));
+            else
+              sts_u4(to, make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                    pack_bf16(o[8 * j + 4], o[8 * j + 5]),
+                                    pack_bf16(o[8 * j + 6], o[8 * j + 7])));
+          }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kRowPieces; ++i) {
+          const int r = i * (32 / kRowPieces) + lane / kRowPieces, pc = lane % kRowPieces;
+          const uint4 v = lds128(stage + r * kRowPieces * 16 + ((pc ^ (r & (kRowPieces - 1))) << 4));
+          const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)orow, r);
+          const bool live = __shfl_sync(0xffffffffu, (int)(row_ok && !(kPart && none)), r) != 0;
+          if (live) {
+            if constexpr (kPart)
+              reinterpret_cast<uint4 *>(a.o_part + (to * a.S + split) * D + c0)[pc] = v;
+            else
+              reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to * D)[pc] = v;
+          }
+        }
+        __syncwarp();
+      };
+      if (a.S > 1) {
+        out_rows(std::true_type{}, 0);
+        out_rows(std::true_type{}, D / 2);
+      } else {
+        out_rows(std::false_type{}, 0);
       }
       if (row_ok) {
         if (a.S > 1) a.lse_part[orow * a.S + split] = lse;
