@@ -198,7 +198,6 @@ struct PrefillArgs {
   float inv_cap;  // 1 / cap_l2
   float cap_r[4]; // capped scores as u R(u^2) for |u| <= cap_u; set by the launch
   float cap_u;
-  float cap_z;
   const float *slopes;
   const int32_t *doc_begin;
   const int32_t *prefix_end;

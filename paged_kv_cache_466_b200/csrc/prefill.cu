@@ -46,15 +46,12 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;   // raise the running max only past this
 constexpr float kQuickMost = 1048576.f;  // largest weight sum of a tile done without a maximum
-// Of every so many pairs of weights one is exponentiated on the FMA pipe.
-constexpr int kExpEvery = 1024, kExpEveryCapped = 1024;
 constexpr int kTile = 128;            // query rows of a tile (the MMA's M)
 constexpr int kKeys = 128;            // keys of a tile
 constexpr int kCtaRows = 2 * kTile;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp0 = 9;
-constexpr int kRing = 4;              // tiles whose page and scale records are kept
 constexpr int kTmemCols = 512;        // scores (P over them) of two row tiles, two outputs
 // Threads, and registers per thread at launch and after the launch's are split
 // anew: a softmax thread holds the 128 scores of its row.
@@ -81,20 +78,26 @@ template <int D, int KVT>
 struct Layout {
   static constexpr int kQBytes = kTile * D * 2;      // one row tile's queries
   static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V tile, bf16
-  static constexpr int kSlots = KVT == PA_KV_BF16 ? 5 : 3;
+  static constexpr int kSlots = (KVT == PA_KV_BF16 ? 5 : 4) * (D == 64 ? 2 : 1);
+  // Tiles whose page and scale records are kept. A loader that writes those of
+  // tile k has seen the slot of K tile k - kSlots / 2 (or, bf16, of the tile
+  // before that one) freed, so the softmax has left the tile before it.
+  static constexpr int kRing = D == 64 ? 8 : 4;
+  static_assert(kRing > kSlots / 2 + 1 || (KVT != PA_KV_BF16 && kRing > kSlots / 2), "records");
   static constexpr int kQOff = 0;
   static constexpr int kSlotOff = 2 * kQBytes;
   // of the last tiles: K scale, K zero, V scale, V zero of every key
   static constexpr int kSzOff = kSlotOff + kSlots * kSlotBytes;
   static constexpr int kSzTile = 4 * kKeys * 4;
   static constexpr int kSzBytes = KVT == PA_KV_BF16 ? 0 : kRing * kSzTile;
-  // quantised pools: per loader warp, 16-key blocks of codes (and the scales
-  // and zeros of their keys) as they come from the pool
-  static constexpr int kRawStages = 3;
+  // quantised pools: per loader warp a 16-key block of codes (and the scales
+  // and zeros of its keys) as it comes from the pool. (A fourth slot instead
+  // of deeper staging: 8192 FP8 tokens 880 us with three slots and three
+  // stages, 699 us with four slots and one.)
   static constexpr int kRawOff = kSzOff + kSzBytes;
   static constexpr int kRawBlock = 16 * (KVT == PA_KV_U4_PER_TOKEN ? D / 2 : D);
   static constexpr int kRawBytes =
-      KVT == PA_KV_BF16 ? 0 : kLoaders<KVT> * kRawStages * (kRawBlock + 256);
+      KVT == PA_KV_BF16 ? 0 : kLoaders<KVT> * (kRawBlock + 256);
   static constexpr int kBarOff = kRawOff + kRawBytes;
   static constexpr int kBytes = kBarOff + 512;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -102,7 +105,7 @@ struct Layout {
 
 // Shared control block behind the tiles.
 struct Control {
-  uint64_t full[5], empty[5];    // K / V slots
+  uint64_t full[10], empty[10];  // K / V slots
   uint64_t q_full;               // queries in shared memory
   uint64_t s_full[2];            // scores of a row tile (and the PV before them) done
   uint64_t p_full[2];            // P of a row tile stored, O rescaled
@@ -110,7 +113,7 @@ struct Control {
   int32_t dead;                  // a bounded wait ran out: everybody stops
   int32_t seq, blk, q0, qlen, ctx;
   int32_t lo, hi;                // first / past-the-last key of any row
-  alignas(8) uint8_t valid[kRing][8];  // per tile: 16-key blocks in valid pages
+  alignas(8) uint8_t valid[8][8];      // per tile: 16-key blocks in valid pages
 };
 static_assert(offsetof(Control, valid) % 8 == 0 && sizeof(Control) <= 512, "control block");
 
@@ -302,43 +305,17 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
 
-// 2^x for a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f
-// by a polynomial (weighted least squares, 2.8e-06 relative error on
-// [-1/2, 1/2]; exactly 1 at 0, so that everything at and below -127 gives
-// exactly 0; 2^127 at and above 127) and n added to the exponent. A share of
-// the weights takes this way because the special-function unit, 16 results per
-// clock and SM, would bound the softmax.
-__device__ __forceinline__ f32x2 exp2_fma(f32x2 x) {
-  float x0, x1;
-  unpack2(x, x0, x1);
-  x = pack2(fminf(fmaxf(x0, -127.f), 127.f), fminf(fmaxf(x1, -127.f), 127.f));
-  const f32x2 magic = pack2(12582912.f, 12582912.f);  // 1.5 * 2^23
-  const f32x2 t = add2(x, magic);
-  const f32x2 f = fma2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
-  f32x2 p = fma2(pack2(0.009582853f, 0.009582853f), f, pack2(0.055906425f, 0.055906425f));
-  p = fma2(p, f, pack2(0.240240986f, 0.240240986f));
-  p = fma2(p, f, pack2(0.693124193f, 0.693124193f));
-  p = fma2(p, f, pack2(1.f, 1.f));
-  float p0, p1, t0, t1;
-  unpack2(p, p0, p1);
-  unpack2(t, t0, t1);
-  p0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  p1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-  return pack2(p0, p1);
-}
-
-// How the scores are changed: not at all, capped, or anything (also a scale
-// that is not positive). The first two let the row maximum be taken before
-// the scores are scaled, as both are increasing functions.
-enum { kPlain = 0, kCapped = 1, kGeneral = 2 };
+// How the scores are changed.
+enum { kCapped = 1, kBiased = 2 };
 
 // ---- the kernel ----------------------------------------------------------------------
 
-template <int D, int KVT, int MODE>
+template <int D, int KVT, int MODE>  // MODE: kCapped | kBiased
 __global__ void __launch_bounds__(kThreads<KVT>, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a) {
   using L = Layout<D, KVT>;
   constexpr bool kQuant = KVT != PA_KV_BF16;
+  constexpr bool kCap = (MODE & kCapped) != 0, kBias = (MODE & kBiased) != 0;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = smem_raw;  // the swizzled tiles need the 1024-byte alignment
   Control &c = *reinterpret_cast<Control *>(smem + L::kBarOff);
@@ -569,7 +546,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
           const int page = past || bad ? a.num_pages : id;  // past the pool: zeros
           if (!is_v && lane < per_tile) {
             if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
-            for (int x = 0; x < a.P / 16; ++x) c.valid[k % kRing][lane * (a.P / 16) + x] = !bad;
+            for (int x = 0; x < a.P / 16; ++x) c.valid[k % L::kRing][lane * (a.P / 16) + x] = !bad;
           }
           const int i = 2 * k + is_v, slot = i % L::kSlots;
           if (i >= L::kSlots)
@@ -617,15 +594,15 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       }
     } else if (n > 0) {
       // ---- quantised pools: the loader warps take the tiles' 16-key blocks in
-      // turn. A block's codes, and the scales and zeros of its keys, are copied
-      // to shared memory kRawStages blocks before they are converted into the
-      // slot; a lane converts what it copied itself.
+      // turn: a block's codes, and the scales and zeros of its keys, are copied
+      // to shared memory while its slot is waited for, and a lane converts what
+      // it copied itself.
       using R = Rows<D, KVT>;
-      constexpr int kSt = L::kRawStages, NW = kLoaders<KVT>;
+      constexpr int NW = kLoaders<KVT>;
       const int w = warp - kLoadWarp0, p_log2 = a.P == 32 ? 5 : 4;
       const int total = n * 2 * (kKeys / 16);
       const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
-      const uint32_t raw0 = sbase + L::kRawOff + w * kSt * (L::kRawBlock + 256);
+      const uint32_t raw = sbase + L::kRawOff + w * (L::kRawBlock + 256);
       auto token_of = [&](int m) { return (t1 - 1 - (m >> 4)) * kKeys + (m & 7) * 16; };
       auto page_of = [&](int m) {  // page of block m; -1: none there, -2: a bad id
         if (m >= total) return -1;
@@ -634,7 +611,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         const int id = __ldg(table + (tok >> p_log2));
         return id < 0 || id >= a.num_pages ? -2 : id;
       };
-      auto fetch = [&](int m, int page, uint32_t raw) {
+      auto fetch = [&](int m, int page) {
         if (m < total) {
           const int tok = token_of(m);
           const int live = page >= 0 ? min(ctx - tok, 16) : 0;
@@ -654,15 +631,18 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         }
         cp_async_commit();
       };
-      // writes block m into its slot; false when the wait for the slot ran out
-      auto put = [&](int m, int page, uint32_t raw) {
+      int page = page_of(w), next = page_of(w + NW);
+      fetch(w, page);
+      for (int m = w; m < total; m += NW) {
         const int i = m >> 3, blk = m & 7, slot = i % L::kSlots;
         const bool is_v = i & 1;
+        const bool bad = page == -2;
         bool ok = true;
         if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        cp_async_wait<0>();
         if (!is_v) {
-          const int ring = (i >> 1) % kRing;
+          const int ring = (i >> 1) % L::kRing;
           float *sz = reinterpret_cast<float *>(smem + L::kSzOff + ring * L::kSzTile) +
                       (lane < 16 ? 0 : 2 * kKeys) + blk * 16 + (lane & 15);
           const uint2 v = lds64(raw + L::kRawBlock + lane * 8);
@@ -671,36 +651,17 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
           sz[0] = x * f;
           sz[kKeys] = fmaf(x, kCodeShift<KVT>, z) * f;
           if (lane == 0) {
-            c.valid[ring][blk] = page != -2;
-            if (page == -2) flag_error(a.d_err, PA_DERR_BAD_PAGE);
+            c.valid[ring][blk] = !bad;
+            if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
           }
         }
         R::store(sbase + L::kSlotOff + slot * L::kSlotBytes, blk, lane, raw);
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&c.full[slot]));
-        return true;
-      };
-      int page[kSt], ahead[kSt];  // of the blocks in flight and of those after them
-#pragma unroll
-      for (int k = 0; k < kSt; ++k) page[k] = page_of(w + NW * k);
-#pragma unroll
-      for (int k = 0; k < kSt; ++k) {
-        fetch(w + NW * k, page[k], raw0 + k * (L::kRawBlock + 256));
-        ahead[k] = page_of(w + NW * (kSt + k));
-      }
-      bool stop = false;
-      for (int m0 = w; m0 < total && !stop; m0 += NW * kSt) {
-#pragma unroll
-        for (int k = 0; k < kSt; ++k) {
-          const int m = m0 + NW * k;
-          const uint32_t raw = raw0 + k * (L::kRawBlock + 256);
-          cp_async_wait<kSt - 1>();
-          if (m < total && !stop) stop = !put(m, page[k], raw);
-          page[k] = ahead[k];
-          fetch(m + NW * kSt, page[k], raw);
-          ahead[k] = page_of(m + 2 * NW * kSt);
-        }
+        page = next;
+        fetch(m + NW, page);
+        next = page_of(m + 2 * NW);
       }
       cp_async_wait<0>();
     }
@@ -728,8 +689,8 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         }
       }
       float slope = 0.f;
-      if constexpr (MODE == kGeneral)
-        if (a.slopes != nullptr && row_ok)
+      if constexpr (kBias)
+        if (row_ok)
           slope = __ldg(a.slopes + orow % a.hq) * 1.4426950408889634f;
       for (int k = 0; k < n; ++k) {
         // (a wait that runs out makes all later ones end at once)
@@ -743,8 +704,8 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         for (int c0 = 0; c0 < kKeys; c0 += 32)
           tmem_ld32(t_s + c0, reinterpret_cast<uint32_t(&)[32]>(s[c0]));
         tmem_wait_ld();
-        const uint32_t sz = sbase + L::kSzOff + k % kRing * L::kSzTile;
-        const uint2 valid = lds64(smem_u32(c.valid[k % kRing]));
+        const uint32_t sz = sbase + L::kSzOff + k % L::kRing * L::kSzTile;
+        const uint2 valid = lds64(smem_u32(c.valid[k % L::kRing]));
         const bool all_valid = valid.x == 0x01010101u && valid.y == 0x01010101u;
         // warp-uniform: every row of the warp sees every key of the tile
         const bool full = __all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kKeys) && all_valid;
@@ -754,10 +715,12 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         // per column. Adds them to lt and, for pools with zeros, p z to zt;
         // returns the largest s^2 with kPoly (else 0).
         float lt, zt;
-        auto weights = [&](auto poly_c, float mul, float m) {
-          constexpr bool kPoly = decltype(poly_c)::value;
-          constexpr int kEvery = kPoly ? kExpEveryCapped : kExpEvery;
-          const f32x2 mul_2 = pack2(mul, mul), neg_2 = pack2(-m, -m);
+        // bias_0, the bias of the tile's first key, and sl, the bias' step from
+        // key to key, are added to x (a quick way of a biased kernel).
+        auto weights = [&](auto poly_c, auto bias_c, float mul, float m, float bias_0, float sl) {
+          constexpr bool kPoly = decltype(poly_c)::value, kAdd = decltype(bias_c)::value;
+          const f32x2 mul_2 = pack2(mul, mul), neg_2 = pack2(bias_0 - m, bias_0 - m);
+          const f32x2 sl_2 = pack2(sl, sl);
           f32x2 l2[2] = {0, 0}, z2 = 0;
           float y4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -770,7 +733,8 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
               for (int i = 0; i < 2; ++i) {
                 const int e = c0 + 2 * (j + i);
                 const f32x2 u = pack2(s[e], s[e + 1]);
-                f32x2 x;
+                f32x2 x = neg_2;
+                if constexpr (kAdd) x = fma2(sl_2, pack2((float)e, (float)(e + 1)), neg_2);
                 if constexpr (kPoly) {
                   const f32x2 y = mul2(u, u);
                   float y0, y1;
@@ -779,17 +743,13 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
                   f32x2 r = pack2(a.cap_r[3], a.cap_r[3]);
 #pragma unroll
                   for (int q = 2; q >= 0; --q) r = fma2(r, y, pack2(a.cap_r[q], a.cap_r[q]));
-                  x = fma2(u, r, neg_2);
+                  x = fma2(u, r, x);
                 } else {
-                  x = fma2(u, mul_2, neg_2);
+                  x = fma2(u, mul_2, x);
                 }
-                if ((j + i) % kEvery == kEvery - 1) {
-                  p[i] = exp2_fma(x);
-                } else {
-                  float x0, x1;
-                  unpack2(x, x0, x1);
-                  p[i] = pack2(fast_exp2(x0), fast_exp2(x1));
-                }
+                float x0, x1;
+                unpack2(x, x0, x1);
+                p[i] = pack2(fast_exp2(x0), fast_exp2(x1));
                 l2[i] = add2(l2[i], p[i]);
               }
               if constexpr (kQuant) {
@@ -847,36 +807,29 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         // kQuickMost (weights above 1 are carried as exactly as those below) and, capped, all
         // scores lie where the polynomial is good. Else the tile is done
         // again, below, from the scores still in registers.
-        bool quick = MODE != kGeneral && full && __all_sync(0xffffffffu, m_run > -INFINITY);
-        if constexpr (MODE != kGeneral) {
-          if (quick) {
-            bool good = true;
-            if constexpr (MODE == kCapped)
-              good = weights(std::true_type{}, mul, m_run) <= a.cap_u * a.cap_u;
-            else
-              weights(std::false_type{}, mul, m_run);
-            quick = __all_sync(0xffffffffu, good && lt < kQuickMost);
-            if (!quick) tmem_wait_st();  // this P is written over
-          }
+        // (a biased tile also needs all its keys before the query: the bias is
+        // then linear in the key)
+        bool quick = full && mul > 0.f && __all_sync(0xffffffffu, m_run > -INFINITY);
+        if constexpr (kBias)
+          quick = quick && (a.prefix_end == nullptr ||
+                            __all_sync(0xffffffffu, !row_ok || pos >= k0 + kKeys - 1));
+        if (quick) {
+          bool good = true;
+          const std::integral_constant<bool, kBias> bias_c{};
+          const float bias_0 = kBias ? slope * (float)(k0 - pos) : 0.f;
+          if constexpr (kCap)
+            good = weights(std::true_type{}, bias_c, mul, m_run, bias_0, slope) <= a.cap_u * a.cap_u;
+          else
+            weights(std::false_type{}, bias_c, mul, m_run, bias_0, slope);
+          quick = __all_sync(0xffffffffu, good && lt < kQuickMost);
+          if (!quick) tmem_wait_st();  // this P is written over
         }
         if (!quick) {
-          if constexpr (MODE == kCapped) {
-            mul = 1.f;
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.cap_z);
-          }
-          if constexpr (MODE == kGeneral) {
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j) s[j] *= mul;
-            mul = 1.f;
-            if (a.cap_l2 > 0.f) {
-#pragma unroll
-              for (int j = 0; j < kKeys; ++j) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
-            }
-            if (a.slopes != nullptr) {
-#pragma unroll
-              for (int j = 0; j < kKeys; ++j) s[j] -= slope * fabsf((float)(pos - k0 - j));
-            }
+          for (int j = 0; j < kKeys; ++j) {
+            s[j] *= mul;
+            if constexpr (kCap) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
+            if constexpr (kBias) s[j] -= slope * fabsf((float)(pos - k0 - j));
           }
           if (!full) {
 #pragma unroll
@@ -893,7 +846,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
           for (int j = 0; j < kKeys; j += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[j + 2 * i], s[j + 2 * i + 1]);
-          const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * mul;
+          const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           const bool need = mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx > -INFINITY);
           if (__any_sync(0xffffffffu, need)) {  // tcgen05.ld / st are warp-wide
             const float m_new = need ? fmaxf(m_run, mx) : m_run;
@@ -913,7 +866,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
               }
             }
           }
-          weights(std::false_type{}, mul, m_run == -INFINITY ? 0.f : m_run);
+          weights(std::false_type{}, std::false_type{}, 1.f, m_run == -INFINITY ? 0.f : m_run, 0.f, 0.f);
         }
         l_run += lt;
         z_run += zt;
@@ -1101,21 +1054,24 @@ cudaError_t launch_mode(const PrefillArgs &a_in, cudaStream_t stream) {
 template <int D, int KVT>
 cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
   PrefillArgs a = a_in;
-  if (a.slopes != nullptr || !(a.scale_log2 > 0.f)) return launch_mode<D, KVT, kGeneral>(a, stream);
-  if (!(a.cap_l2 > 0.f)) return launch_mode<D, KVT, kPlain>(a, stream);
-  // cap tanh(z), z = cap_z u, as u R(u^2)
-  // u is q.k (bf16 pools) or the score in log2 units
+  // cap tanh(z), z = cap_z u, as u R(u^2), fitted for the least absolute error
+  // of tanh, 1.9e-7, on |z| <= 1/2; u is q.k (bf16 pools) or the score in log2
+  // units. Coefficients that fp32 cannot hold (a tiny cap or scale) leave the
+  // bound at 0: such scores take the other way.
   const double z = KVT == PA_KV_BF16 ? (double)a.scale_log2 * a.inv_cap : (double)a.inv_cap;
-  // (fitted for the least absolute error, 1.9e-7, on |z| <= 1/2)
   const double c[4] = {1.0, -0.333264608, 0.131858621, -0.044229293};
   double zz = z;
-  for (int i = 0; i < 4; ++i, zz *= z * z) a.cap_r[i] = (float)(a.cap_l2 * c[i] * zz);
-  a.cap_z = (float)z;
-  a.cap_u = (float)(0.5 / z);
-  // coefficients that fp32 cannot hold (a tiny cap or scale) leave the other way
-  for (int i = 0; i < 4; ++i)
-    if (!std::isfinite(a.cap_r[i]) || !std::isfinite(a.cap_u)) return launch_mode<D, KVT, kGeneral>(a, stream);
-  return launch_mode<D, KVT, kCapped>(a, stream);
+  bool fits = a.cap_l2 > 0.f && z > 0.0 && 0.5 / z < 1e18;  // (the bound is used squared)
+  for (int i = 0; i < 4; ++i, zz *= z * z) {
+    a.cap_r[i] = (float)(a.cap_l2 * c[i] * zz);
+    fits = fits && std::isfinite(a.cap_r[i]);
+  }
+  a.cap_u = fits ? (float)(0.5 / z) : 0.f;
+  if (a.slopes != nullptr)
+    return a.cap_l2 > 0.f ? launch_mode<D, KVT, kCapped | kBiased>(a, stream)
+                          : launch_mode<D, KVT, kBiased>(a, stream);
+  return a.cap_l2 > 0.f ? launch_mode<D, KVT, kCapped>(a, stream)
+                        : launch_mode<D, KVT, 0>(a, stream);
 }
 
 }  // namespace
