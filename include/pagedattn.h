@@ -392,10 +392,12 @@ typedef struct {
  *              every axis. A position outside [0, table_len) flags
  *              PA_DERR_BAD_POS; that sequence stores nothing and gets out = 0
  *   k_new, v_new : as for pa_decode_append, or both NULL: nothing is written
- * Other arguments, the workspace and the split count as for pa_decode_append;
- * with every change NULL the result is pa_decode_append's (or pa_decode's),
- * bit for bit. With rope, the stored row and the result are those of
- * pa_kv_append_rope followed by a call without rope, k_new and v_new.
+ * Other arguments, the workspace and the split count as for pa_decode_append.
+ * With rope, the stored row and the result are those of pa_kv_append_rope
+ * followed by a call without rope, k_new and v_new, bit for bit. (With every
+ * change NULL it computes what pa_decode_append or pa_decode does; the bits of
+ * the output may differ: codes enter centred and block sums are added rounded,
+ * so that long contexts do not drift.)
  */
 pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
                              const pa_rope_t *rope, const void *q, const void *k_new,

@@ -459,6 +459,27 @@ struct WarpAcc {
   }
 };
 
+// Where the products of a block are summed. The tensor core cuts its sums off
+// toward zero, which over a long context adds up to a drift of O (8.8e-6 of it
+// after 230 blocks of a warp, and a multiple of that where zero points cancel
+// most of O). kFresh: a block's products are summed from zero and added to O
+// by a rounded addition; else they are accumulated in place.
+template <bool kFresh>
+struct Accumulator {
+  float (&v)[4];
+  __device__ __forceinline__ explicit Accumulator(float (&o)[4]) : v(o) {}
+};
+template <>
+struct Accumulator<true> {
+  float (&o)[4];
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ explicit Accumulator(float (&o_)[4]) : o(o_) {}
+  __device__ __forceinline__ ~Accumulator() {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += v[e];
+  }
+};
+
 // Scores, online softmax and O^T update for the 16-token bf16 block staged at
 // `src`, whose first token is btok; tokens outside [tok_lo, tok1) and all
 // tokens of an invalid page (pvalid false) are masked.
@@ -537,6 +558,12 @@ __device__ __forceinline__ void block_step(const LaneMap<D, PA_KV_BF16> &lm, uin
   uint32_t bh0, bl0, bh1, bl1;
   split_bf16(p[0], p[1], bh0, bl0);
   split_bf16(p[2], p[3], bh1, bl1);
+  // MOD: what is left is a third operand, so that a weight's 24 bits all count
+  uint32_t br0 = 0, br1 = 0;
+  if constexpr (MOD) {
+    br0 = pack_bf16(p[0] - bf16_lo(bh0) - bf16_lo(bl0), p[1] - bf16_hi(bh0) - bf16_hi(bl0));
+    br1 = pack_bf16(p[2] - bf16_lo(bh1) - bf16_lo(bl1), p[3] - bf16_hi(bh1) - bf16_hi(bl1));
+  }
 #pragma unroll
   for (int c = 0; c < T::kVChunks; ++c) {
     const uint4 v0 = lds128(src + voff[0][c]);
@@ -553,8 +580,10 @@ __device__ __forceinline__ void block_step(const LaneMap<D, PA_KV_BF16> &lm, uin
       const uint32_t a1 = __byte_perm(x0[w], x1[w], 0x7632);
       const uint32_t a2 = __byte_perm(x2[w], x3[w], 0x5410);
       const uint32_t a3 = __byte_perm(x2[w], x3[w], 0x7632);
-      mma_bf16_16816(o[4 * c + w], a0, a1, a2, a3, bh0, bh1);
-      mma_bf16_16816(o[4 * c + w], a0, a1, a2, a3, bl0, bl1);
+      Accumulator<MOD> d(o[4 * c + w]);
+      mma_bf16_16816(d.v, a0, a1, a2, a3, bh0, bh1);
+      mma_bf16_16816(d.v, a0, a1, a2, a3, bl0, bl1);
+      if constexpr (MOD) mma_bf16_16816(d.v, a0, a1, a2, a3, br0, br1);
     }
   }
 }
@@ -619,6 +648,35 @@ struct QAcc {
   }
 };
 
+// V codes less the middle of their range (kCentre, MOD): O is then a sum of
+// small terms of both signs instead of one that cancels the zero points' (K's
+// sums run over head_dim terms only and cancel little). Exact in f16: 1024 + c
+// is a bit pattern away.
+template <int KVT>
+constexpr float kCentre = KVT == PA_KV_U8_PER_TOKEN ? 128.f : KVT == PA_KV_U4_PER_TOKEN ? 8.f : 0.f;
+
+__device__ __forceinline__ uint32_t f16x2_add(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// INT8: the two bytes that `sel` picks (its high bytes pick 0x64).
+__device__ __forceinline__ uint32_t u8x2_centred(uint32_t word, uint32_t sel) {
+  return f16x2_add(__byte_perm(word, 0x64646464u, sel), 0xE480E480u);  // - 1152
+}
+// INT4: low nibbles of the two 16-bit halves, and high nibbles of their low bytes.
+__device__ __forceinline__ uint32_t u4x2_low(uint32_t w) {
+  return f16x2_add((w & 0x000F000Fu) | 0x64006400u, 0xE408E408u);  // - 1032
+}
+__device__ __forceinline__ uint32_t u4x2_high(uint32_t w) {
+  return f16x2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+}
+
 // S^T of the 16-token quantised block staged at `src` (codes times the
 // Tile's power of two): s[0], s[1] = token g, heads 2t, 2t + 1; s[2], s[3] =
 // token g + 8.
@@ -681,7 +739,7 @@ __device__ __forceinline__ void scores_t(const LaneMap<D, KVT> &lm, uint32_t src
 
 // O^T += V^T W^T for the quantised block staged at `src`, with the weights'
 // B fragments (hi and lo halves, tokens 0..7 in b?0 and 8..15 in b?1).
-template <int D, int KVT, bool kTwo = true>
+template <int D, int KVT, bool MOD, bool kTwo = true>
 __device__ __forceinline__ void pv_quant(const LaneMap<D, KVT> &lm, uint32_t src, int g,
                                          uint32_t bh0, uint32_t bh1, uint32_t bl0,
                                          uint32_t bl1, float (&o)[D / 16][4]) {
@@ -711,14 +769,17 @@ __device__ __forceinline__ void pv_quant(const LaneMap<D, KVT> &lm, uint32_t src
       const uint32_t ya = __byte_perm(xv[0][j / 4], xv[1][j / 4], sel);
       const uint32_t yb = __byte_perm(xv[2][j / 4], xv[3][j / 4], sel);
       const uint32_t ya8 = ya >> 8, yb8 = yb >> 8;
-      const uint32_t a0[2] = {ya & 0x000F000Fu, ya8 & 0x000F000Fu};
-      const uint32_t a1[2] = {ya & 0x00F000F0u, ya8 & 0x00F000F0u};
-      const uint32_t a2[2] = {yb & 0x000F000Fu, yb8 & 0x000F000Fu};
-      const uint32_t a3[2] = {yb & 0x00F000F0u, yb8 & 0x00F000F0u};
+      auto lo = [](uint32_t w) { return MOD ? u4x2_low(w) : w & 0x000F000Fu; };
+      auto hi = [](uint32_t w) { return MOD ? u4x2_high(w) : w & 0x00F000F0u; };
+      const uint32_t a0[2] = {lo(ya), lo(ya8)};
+      const uint32_t a1[2] = {hi(ya), hi(ya8)};
+      const uint32_t a2[2] = {lo(yb), lo(yb8)};
+      const uint32_t a3[2] = {hi(yb), hi(yb8)};
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        mma_f16_16816(o[j + u], a0[u], a1[u], a2[u], a3[u], bh0, bh1);
-        if constexpr (kTwo) mma_f16_16816(o[j + u], a0[u], a1[u], a2[u], a3[u], bl0, bl1);
+        Accumulator<MOD> d(o[j + u]);
+        mma_f16_16816(d.v, a0[u], a1[u], a2[u], a3[u], bh0, bh1);
+        if constexpr (kTwo) mma_f16_16816(d.v, a0[u], a1[u], a2[u], a3[u], bl0, bl1);
       }
     }
   } else {
@@ -740,12 +801,16 @@ __device__ __forceinline__ void pv_quant(const LaneMap<D, KVT> &lm, uint32_t src
       const uint32_t w3 = D == 128 ? x3[j / 2] : ((g & 1) ? x3[2 + j / 2] : x3[j / 2]);
       const uint32_t xa = __byte_perm(w0, w1, sel);
       const uint32_t xb = __byte_perm(w2, w3, sel);
-      const uint32_t a0 = kIsFp8<KVT> ? e4m3x2_to_f16x2(xa) : u8x2_to_f16x2(xa, 0x4140);
-      const uint32_t a1 = kIsFp8<KVT> ? e4m3x2_hi_to_f16x2(xa) : u8x2_to_f16x2(xa, 0x4342);
-      const uint32_t a2 = kIsFp8<KVT> ? e4m3x2_to_f16x2(xb) : u8x2_to_f16x2(xb, 0x4140);
-      const uint32_t a3 = kIsFp8<KVT> ? e4m3x2_hi_to_f16x2(xb) : u8x2_to_f16x2(xb, 0x4342);
-      mma_f16_16816(o[j], a0, a1, a2, a3, bh0, bh1);
-      if constexpr (kTwo) mma_f16_16816(o[j], a0, a1, a2, a3, bl0, bl1);
+      auto two = [](uint32_t word, bool upper) {
+        if constexpr (kIsFp8<KVT>) return upper ? e4m3x2_hi_to_f16x2(word) : e4m3x2_to_f16x2(word);
+        else if constexpr (MOD) return u8x2_centred(word, upper ? 0x4342 : 0x4140);
+        else return u8x2_to_f16x2(word, upper ? 0x4342 : 0x4140);
+      };
+      const uint32_t a0 = two(xa, false), a1 = two(xa, true);
+      const uint32_t a2 = two(xb, false), a3 = two(xb, true);
+      Accumulator<MOD> d(o[j]);
+      mma_f16_16816(d.v, a0, a1, a2, a3, bh0, bh1);
+      if constexpr (kTwo) mma_f16_16816(d.v, a0, a1, a2, a3, bl0, bl1);
     }
   }
 }
@@ -792,6 +857,10 @@ __device__ __forceinline__ void pair_step(const LaneMap<D, KVT> &lm, uint32_t sr
     vz[u][0] = __uint_as_float(v0.y);
     vs[u][1] = __uint_as_float(v1.x);
     vz[u][1] = __uint_as_float(v1.y);
+    if constexpr (MOD) {
+      vz[u][0] = fmaf(vs[u][0], kCentre<KVT>, vz[u][0]);
+      vz[u][1] = fmaf(vs[u][1], kCentre<KVT>, vz[u][1]);
+    }
     if (!(pvalid[u] && btok[u] >= tok_lo && btok[u] + 16 <= tok1)) {  // warp-uniform
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -903,11 +972,11 @@ __device__ __forceinline__ void pair_step(const LaneMap<D, KVT> &lm, uint32_t sr
       // lanes t - 2), and one MMA per m-tile does both
       const uint32_t x0 = __shfl_xor_sync(0xffffffffu, l0, 2);
       const uint32_t x1 = __shfl_xor_sync(0xffffffffu, l1, 2);
-      pv_quant<D, KVT, false>(lm, src + u * T::kStageBytes, g,
+      pv_quant<D, KVT, MOD, false>(lm, src + u * T::kStageBytes, g,
                               movmatrix_trans(t < 2 ? h0 : x0),
                               movmatrix_trans(t < 2 ? h1 : x1), 0u, 0u, acc.o);
     } else {
-      pv_quant<D, KVT>(lm, src + u * T::kStageBytes, g, movmatrix_trans(h0),
+      pv_quant<D, KVT, MOD>(lm, src + u * T::kStageBytes, g, movmatrix_trans(h0),
                        movmatrix_trans(h1), movmatrix_trans(l0), movmatrix_trans(l1), acc.o);
     }
   }
@@ -1295,6 +1364,7 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
     // sums of q of heads 2t, 2t + 1 (held by lanes 8t and 8t + 4)
     const float qz[2] = {__shfl_sync(0xffffffffu, qsum, 8 * t) * a.scale_log2,
                          __shfl_sync(0xffffffffu, qsum, 8 * t + 4) * a.scale_log2};
+    constexpr float kScale = MOD ? 1.f : kCodeScale<KVT>;  // of the V codes
     const float kscale = kCodeScale<KVT> * a.scale_log2;
     // one range through the warp's ring; the online softmax state carries over
     auto pass = [&](auto pack_c, const Range &r) {
@@ -1351,7 +1421,7 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
     // holding their tokens, then O = (code scale * 2^E * O + sum p z) / l
     // (the code scale is applied to O first: code scale x 2^E alone may pass
     // the fp32 range when E is large)
-    constexpr float kRowHiScale = T::kU4 ? kCodeScale<KVT> / 16.f : kCodeScale<KVT>;
+    constexpr float kRowHiScale = T::kU4 && !MOD ? kScale / 16.f : kScale;
     float pe[2], zl[2];
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -1375,10 +1445,10 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
       const int d0 = out_col<D, KVT>(j, g);
       // rows d + 1 of INT4 tiles hold the high nibbles (16x the code scale)
       *reinterpret_cast<float2 *>(rec_o + (2 * t) * D + d0) =
-          make_float2(fmaf(acc.o[j][0] * kCodeScale<KVT>, pe[0], zl[0]),
+          make_float2(fmaf(acc.o[j][0] * kScale, pe[0], zl[0]),
                       fmaf(acc.o[j][2] * kRowHiScale, pe[0], zl[0]));
       *reinterpret_cast<float2 *>(rec_o + (2 * t + 1) * D + d0) =
-          make_float2(fmaf(acc.o[j][1] * kCodeScale<KVT>, pe[1], zl[1]),
+          make_float2(fmaf(acc.o[j][1] * kScale, pe[1], zl[1]),
                       fmaf(acc.o[j][3] * kRowHiScale, pe[1], zl[1]));
     }
   }

@@ -2,11 +2,11 @@
 the cache write in the same launch, against the definition in 64 bits.
 
 Tolerance. A weight is exp(x): its relative error is the error of x, plus the
-2^-17 of the residual half of the split weights and the 2^-22 of ex2. x carries
-the fp32 accumulation of q.k (at most D / 16 + 8 roundings of 2^-23 of
-s_abs = scale sum |q||k|), the cap's (2^-22 cap), the bias' (three roundings
-of the bias of the keys that matter, below 32). Numerator and denominator each
-carry it once, against values up to max|v|:
+2^-17 that a weight cut to two 16-bit halves may lose (none does here) and the
+2^-22 of ex2. x carries the fp32 accumulation of q.k (at most D / 16 + 8
+roundings of 2^-23 of s_abs = scale sum |q||k|), the cap's (2^-22 cap), the
+bias' (three roundings of the bias of the keys that matter, below 32).
+Numerator and denominator each carry it once, against values up to max|v|:
   |err| <= 2 max|v| (2^-17 + 2^-22 + 2^-23 (D / 16 + 8) s_abs + 2^-22 cap + 3 * 32 * 2^-24)
 The errors of single keys are independent, so in the 2-norm they stay within
 2e-5 of the result (the largest, 2^-17, is 7.6e-6).
@@ -17,8 +17,7 @@ import pytest
 import torch
 
 from paged_kv_cache_466_b200 import (PA_DERR_BAD_CTX, PA_DERR_BAD_PAGE, PA_DERR_BAD_POS, Rope, _lib,
-                                     pa_decode, pa_decode_append, pa_decode_num_splits,
-                                     pa_decode_scored, pa_decode_workspace_bytes, pa_kv_append_rope)
+                                     pa_decode_append, pa_decode_scored, pa_decode_workspace_bytes, pa_kv_append_rope)
 from paged_kv_cache_466_b200._lib import (PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE,
                                           PA_OK, pa_kv_pool_t, pa_rope_t, pa_score_t)
 from tests.helpers import DEV
@@ -104,17 +103,33 @@ def test_large_scores_reach_the_cap(kind):
 
 
 @gpu
-@pytest.mark.parametrize("kind", ["bf16", "u4"])
-def test_without_changes_it_is_the_plain_decode(kind):
+@pytest.mark.parametrize("kind", ["bf16", "u8", "fp8", "u4"])
+def test_without_changes_it_attends_as_the_plain_decode(kind):
+    """No change of the scores: the plain decode's definition; the stored rows are its bits."""
     lens = [5, 300, 1, 64]
     pool, bt, ctx, g = make_batch(lens, 8, 2, 128, 16, kind)
+    other, _, _, _ = make_batch(lens, 8, 2, 128, 16, kind)
     q = torch.randn(4, 8, 128, generator=g, device=DEV).to(torch.bfloat16)
     k, v = (torch.randn(4, 2, 128, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
     for S in (1, 2):
-        assert torch.equal(pa_decode_scored(pool, q, bt, ctx, 0.1, num_splits=S),
-                           pa_decode(pool, q, bt, ctx, 0.1, num_splits=S))
-        assert torch.equal(pa_decode_scored(pool, q, bt, ctx, 0.1, k_new=k, v_new=v, num_splits=S),
-                           pa_decode_append(pool, q, k, v, bt, ctx, 0.1, num_splits=S))
+        _check(pool, q, bt, ctx, 0.1, pa_decode_scored(pool, q, bt, ctx, 0.1, num_splits=S))
+        got = pa_decode_scored(pool, q, bt, ctx, 0.1, k_new=k, v_new=v, num_splits=S)
+        pa_decode_append(other, q, k, v, bt, ctx, 0.1, num_splits=S)
+        _check(other, q, bt, ctx, 0.1, got)
+        for x, y in zip(pool.tensors(), other.tensors()):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8", "fp8", "u4"])
+def test_long_contexts_do_not_drift(kind):
+    """30,000 tokens in as few splits as there can be: sums of blocks are added rounded, not
+    cut off, and zero points do not cancel most of the output (codes enter centred)."""
+    pool, bt, ctx, g = make_batch([30000, 12345], 8, 1, 64, 32, kind, seed=2)
+    q = torch.randn(2, 8, 64, generator=g, device=DEV).to(torch.bfloat16)
+    for cap in (0.0, 30.0):
+        _check(pool, q, bt, ctx, 0.125, pa_decode_scored(pool, q, bt, ctx, 0.125, softcap=cap, num_splits=1),
+               softcap=cap)
 
 
 @gpu
