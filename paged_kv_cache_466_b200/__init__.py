@@ -80,6 +80,12 @@ except AttributeError:  # pragma: no cover
     _raw_stream = None
 
 
+try:
+    _current_device = torch._C._cuda_getDevice
+except AttributeError:  # pragma: no cover
+    _current_device = torch.cuda.current_device
+
+
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
@@ -89,6 +95,8 @@ def _stream(stream=None):
 
 
 def _need(t: torch.Tensor, name: str, dtype, device=None):
+    if t.dtype is dtype and t.is_contiguous() and (device is None or t.device == device):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -99,7 +107,7 @@ def _need(t: torch.Tensor, name: str, dtype, device=None):
 
 def _need_device(device, where: str, d_err: Optional[torch.Tensor]):
     """The call runs on the current device: the pool must be there, and the error word."""
-    if device.type != "cuda" or device.index not in (None, torch.cuda.current_device()):
+    if device.type != "cuda" or device.index != _current_device():
         raise ValueError(f"{where}: the pool is on {device}, not on the current CUDA device")
     if d_err is not None:
         _need(d_err, "d_err", torch.int32, device)
@@ -242,15 +250,17 @@ def pa_kv_append(pool: KVPool, k_new: torch.Tensor, v_new: torch.Tensor, seq_idx
 
 def _token_rows(t: torch.Tensor, name: str, heads: int, dim: int, device) -> int:
     """Elements between the tokens of bf16 [N, heads, dim], each token's rows dense."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is torch.bfloat16 and len(shape) == 3 and shape[1] == heads and shape[2] == dim \
+            and stride[2] == 1 and (heads == 1 or stride[1] == dim) and t.device == device:
+        return stride[0] if shape[0] > 1 else heads * dim
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    raise ValueError(f"{name}: the heads of a token must be contiguous")
 
 
 def pa_kv_append_rope(pool: KVPool, rope: Rope, q: Optional[torch.Tensor], k_new: torch.Tensor,
@@ -279,8 +289,9 @@ def pa_kv_append_rope(pool: KVPool, rope: Rope, q: Optional[torch.Tensor], k_new
         hq = q.shape[1] if q.dim() == 3 else 0
         qs = _token_rows(q, "q", hq, D, dev)
         if q_out is None:
-            q_out = torch.empty((q.shape[0], hq, D), dtype=torch.bfloat16, device=dev)
-        _need(q_out, "q_out", torch.bfloat16, dev)
+            q_out = q.new_empty(q.shape)
+        else:
+            _need(q_out, "q_out", torch.bfloat16, dev)
         if q.shape[0] != n or q_out.shape != q.shape:
             raise ValueError("pa_kv_append_rope: shape mismatch")
     if rope_pos is not None:
@@ -438,10 +449,11 @@ def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
             raise ValueError("pa_decode_scored: rope_pos must be [num_axes, sequences] of a rope")
     score = _score(softcap, alibi_slopes, Hq, doc_begin, None, B, dev)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
-    _need(out, "out", torch.float32, dev)
-    if tuple(out.shape) != (B, Hq, D):
-        raise ValueError("pa_decode_scored: out must be [B, Hq, D]")
+        out = q.new_empty((B, Hq, D), dtype=torch.float32)
+    else:
+        _need(out, "out", torch.float32, dev)
+        if out.shape != q.shape:
+            raise ValueError("pa_decode_scored: out must be [B, Hq, D]")
     max_pages = block_tables.shape[1]
     if workspace is None:
         need = pa_decode_workspace_bytes(B, Hq, D,
@@ -491,10 +503,11 @@ def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_table
         raise ValueError("pa_prefill: shape mismatch")
     score = _score(softcap, alibi_slopes, Hq, doc_begin, prefix_end, N, dev)
     if out is None:
-        out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev)
-    if tuple(out.shape) != (N, Hq, D):
-        raise ValueError("pa_prefill: out must be [N, Hq, D]")
+        out = q.new_empty((N, Hq, D))
+    else:
+        _need(out, "out", torch.bfloat16, dev)
+        if out.shape != q.shape:
+            raise ValueError("pa_prefill: out must be [N, Hq, D]")
     if lse_out is not None:
         _need(lse_out, "lse_out", torch.float32, dev)
         if tuple(lse_out.shape) != (N, Hq):
