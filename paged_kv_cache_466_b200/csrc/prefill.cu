@@ -62,9 +62,9 @@ constexpr int kLoaders = kThreads<KVT> / 32 - kLoadWarp0;  // warps (bf16 pools 
 template <int KVT>
 constexpr int kLaunchRegs = KVT == PA_KV_BF16 ? 168 : 128;
 template <int KVT>
-constexpr int kSoftmaxRegs = KVT == PA_KV_BF16 ? 224 : 208;
+constexpr int kSoftmaxRegs = KVT == PA_KV_BF16 ? 224 : 200;
 template <int KVT>
-constexpr int kOtherRegs = KVT == PA_KV_BF16 ? 56 : 48;
+constexpr int kOtherRegs = 56;
 template <int KVT>
 constexpr int kSplitRegs = kSoftmaxRegs<KVT> * kSoftmaxThreads +
                            kOtherRegs<KVT> * (kThreads<KVT> - kSoftmaxThreads);
@@ -235,21 +235,23 @@ struct Rows {
                       u4x2_to_bf16(w >> 12));
   }
   static __device__ __forceinline__ void store(uint32_t tile, int blk, int lane, uint32_t raw) {
+    uint4 v[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) v[k] = lds128(raw + (lane + 32 * k) * 16);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       const int at = (lane + 32 * k) * 16;
       const int r = blk * 16 + at / kRowBytes;
-      const uint4 v = lds128(raw + at);
       if constexpr (KVT == PA_KV_U4_PER_TOKEN) {
         const int c0 = at % kRowBytes / 4;  // four 16-byte chunks of bf16
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) sts_u4(tile + sw128(r, c0 + j, kKeys), convert8(w[j]));
       } else {
         // lanes of the second 64 columns write their chunks in the other order:
         // both halves' chunks would share banks
         const int pc = at % kRowBytes / 16, o = (pc >> 2) & 1;
-        const uint4 a = convert8(v.x, v.y), b = convert8(v.z, v.w);
+        const uint4 a = convert8(v[k].x, v[k].y), b = convert8(v[k].z, v[k].w);
         sts_u4(tile + sw128(r, 2 * pc + o, kKeys), o ? b : a);
         sts_u4(tile + sw128(r, 2 * pc + 1 - o, kKeys), o ? a : b);
       }
@@ -460,6 +462,78 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
   const uint32_t tmem = c.tmem;
   volatile int32_t *dead = &c.dead;
 
+  // With one row tile the other tile's softmax warps help with the codes.
+  const int NW = kLoaders<KVT> + (subs == 1 ? 4 : 0);
+  auto load_codes = [&](int w, uint32_t raw) {
+    // ---- quantised pools: the loader warps (w of NW) take the tiles' 16-key
+    // blocks in turn: a block's codes, and the scales and zeros of its keys, are copied
+    // to shared memory while its slot is waited for, and a lane converts what
+    // it copied itself.
+    using R = Rows<D, KVT>;
+    const int p_log2 = a.P == 32 ? 5 : 4;
+    const int total = n * 2 * (kKeys / 16);
+    const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
+    auto token_of = [&](int m) { return (t1 - 1 - (m >> 4)) * kKeys + (m & 7) * 16; };
+    auto there = [&](int m) { return m < total && token_of(m) < ctx; };
+    // the table's entry for block m, not looked at yet (the load is waited
+    // for where it is used, a block later)
+    auto entry_of = [&](int m) { return there(m) ? __ldg(table + (token_of(m) >> p_log2)) : 0; };
+    auto fetch = [&](int m, int page) {
+      if (m < total) {
+        const int tok = token_of(m);
+        const bool good = there(m) && page >= 0 && page < a.num_pages;
+        const int live = good ? min(ctx - tok, 16) : 0;
+        const bool is_v = (m >> 3) & 1;
+        const size_t row0 = (((size_t)(good ? page : 0) * a.hkv + h) << p_log2) + (tok & (a.P - 1));
+        const unsigned char *src =
+            static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool) + row0 * R::kRowBytes;
+#pragma unroll
+        for (int k = 0; k < R::kPieces; ++k) {
+          const int at = (lane + 32 * k) * 16;
+          cp_async16(raw + at, src + at, at / R::kRowBytes < live ? 16u : 0u);
+        }
+        if (!is_v)
+          cp_async8(raw + L::kRawBlock + lane * 8,
+                    reinterpret_cast<const float2 *>(lane < 16 ? a.k_sz : a.v_sz) + row0 + (lane & 15),
+                    (lane & 15) < live ? 8u : 0u);
+      }
+      cp_async_commit();
+    };
+    int page = entry_of(w), next = entry_of(w + NW);
+    fetch(w, page);
+    for (int m = w; m < total; m += NW) {
+      const int i = m >> 3, blk = m & 7, slot = i % L::kSlots;
+      const bool is_v = i & 1;
+      const bool bad = there(m) && (page < 0 || page >= a.num_pages);
+      bool ok = true;
+      if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      cp_async_wait<0>();
+      if (!is_v) {
+        const int ring = (i >> 1) % L::kRing;
+        float *sz = reinterpret_cast<float *>(smem + L::kSzOff + ring * L::kSzTile) +
+                    (lane < 16 ? 0 : 2 * kKeys) + blk * 16 + (lane & 15);
+        const uint2 v = lds64(raw + L::kRawBlock + lane * 8);
+        const float x = __uint_as_float(v.x), z = __uint_as_float(v.y);
+        const float f = lane < 16 ? a.scale_log2 : 1.f;  // K rows carry the score scale
+        sz[0] = x * f;
+        sz[kKeys] = fmaf(x, kCodeShift<KVT>, z) * f;
+        if (lane == 0) {
+          c.valid[ring][blk] = !bad;
+          if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
+        }
+      }
+      R::store(sbase + L::kSlotOff + slot * L::kSlotBytes, blk, lane, raw);
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&c.full[slot]));
+      page = next;
+      fetch(m + NW, page);
+      next = entry_of(m + 2 * NW);
+    }
+    cp_async_wait<0>();
+  };
+
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<KVT>));
     if (warp == kMmaWarp) {
@@ -593,77 +667,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         }
       }
     } else if (n > 0) {
-      // ---- quantised pools: the loader warps take the tiles' 16-key blocks in
-      // turn: a block's codes, and the scales and zeros of its keys, are copied
-      // to shared memory while its slot is waited for, and a lane converts what
-      // it copied itself.
-      using R = Rows<D, KVT>;
-      constexpr int NW = kLoaders<KVT>;
-      const int w = warp - kLoadWarp0, p_log2 = a.P == 32 ? 5 : 4;
-      const int total = n * 2 * (kKeys / 16);
-      const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
-      const uint32_t raw = sbase + L::kRawOff + w * (L::kRawBlock + 256);
-      auto token_of = [&](int m) { return (t1 - 1 - (m >> 4)) * kKeys + (m & 7) * 16; };
-      auto page_of = [&](int m) {  // page of block m; -1: none there, -2: a bad id
-        if (m >= total) return -1;
-        const int tok = token_of(m);
-        if (tok >= ctx) return -1;
-        const int id = __ldg(table + (tok >> p_log2));
-        return id < 0 || id >= a.num_pages ? -2 : id;
-      };
-      auto fetch = [&](int m, int page) {
-        if (m < total) {
-          const int tok = token_of(m);
-          const int live = page >= 0 ? min(ctx - tok, 16) : 0;
-          const bool is_v = (m >> 3) & 1;
-          const size_t row0 = (((size_t)max(page, 0) * a.hkv + h) << p_log2) + (tok & (a.P - 1));
-          const unsigned char *src =
-              static_cast<const unsigned char *>(is_v ? a.v_pool : a.k_pool) + row0 * R::kRowBytes;
-#pragma unroll
-          for (int k = 0; k < R::kPieces; ++k) {
-            const int at = (lane + 32 * k) * 16;
-            cp_async16(raw + at, src + at, at / R::kRowBytes < live ? 16u : 0u);
-          }
-          if (!is_v)
-            cp_async8(raw + L::kRawBlock + lane * 8,
-                      reinterpret_cast<const float2 *>(lane < 16 ? a.k_sz : a.v_sz) + row0 + (lane & 15),
-                      (lane & 15) < live ? 8u : 0u);
-        }
-        cp_async_commit();
-      };
-      int page = page_of(w), next = page_of(w + NW);
-      fetch(w, page);
-      for (int m = w; m < total; m += NW) {
-        const int i = m >> 3, blk = m & 7, slot = i % L::kSlots;
-        const bool is_v = i & 1;
-        const bool bad = page == -2;
-        bool ok = true;
-        if (i >= L::kSlots) ok = wait_bar(smem_u32(&c.empty[slot]), (i / L::kSlots - 1) & 1, dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        cp_async_wait<0>();
-        if (!is_v) {
-          const int ring = (i >> 1) % L::kRing;
-          float *sz = reinterpret_cast<float *>(smem + L::kSzOff + ring * L::kSzTile) +
-                      (lane < 16 ? 0 : 2 * kKeys) + blk * 16 + (lane & 15);
-          const uint2 v = lds64(raw + L::kRawBlock + lane * 8);
-          const float x = __uint_as_float(v.x), z = __uint_as_float(v.y);
-          const float f = lane < 16 ? a.scale_log2 : 1.f;  // K rows carry the score scale
-          sz[0] = x * f;
-          sz[kKeys] = fmaf(x, kCodeShift<KVT>, z) * f;
-          if (lane == 0) {
-            c.valid[ring][blk] = !bad;
-            if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
-          }
-        }
-        R::store(sbase + L::kSlotOff + slot * L::kSlotBytes, blk, lane, raw);
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_u32(&c.full[slot]));
-        page = next;
-        fetch(m + NW, page);
-        next = page_of(m + 2 * NW);
-      }
-      cp_async_wait<0>();
+      load_codes(warp - kLoadWarp0, sbase + L::kRawOff + (warp - kLoadWarp0) * (L::kRawBlock + 256));
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<KVT>));
@@ -675,6 +679,11 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     const uint32_t t_o = tmem + 2 * kKeys + sub * D + lane_off;
     float m_run = -INFINITY, l_run = 0.f, z_run = 0.f;
     bool ok = true;
+    if constexpr (kQuant) {
+      if (sub >= subs && n > 0)  // (in the place of the other row tile's queries)
+        load_codes(kLoaders<KVT> + warp - 4,
+                   sbase + L::kQOff + L::kQBytes + (warp - 4) * (L::kRawBlock + 256));
+    }
     if (sub < subs && n > 0) {
       constexpr bool kZero = kQuant && KVT != PA_KV_FP8_PER_TOKEN;  // rows have a zero point
       float qsum = 0.f;
