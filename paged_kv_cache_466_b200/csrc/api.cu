@@ -688,6 +688,10 @@ namespace {
 // Key splits of pa_prefill: with fewer (256-row block, KV head) units than
 // SMs, as many as fill the SMs once, each of at least four 128-key tiles.
 // The blocks are estimated from the token count, the keys from the table width.
+// (More splits than that, to even out the last wave, were slower: 512-token
+// chunks of two sequences over 32,000 bf16 tokens, 64/8 heads, 256 CTAs on 148
+// SMs, 1001 us at one split and 1108 at four: blocks of a head that walk the
+// keys together share them in the L2.)
 int prefill_splits(const pa_kv_pool_t *pool, int n, int B, int hq, int max_pages, int requested) {
   const long long tiles = ((long long)max_pages * pool->page_size + 127) / 128;
   long long S = requested;

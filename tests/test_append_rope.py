@@ -123,6 +123,22 @@ def test_extreme_magnitudes(scale):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["u8", "fp8", "u4"])
+@pytest.mark.parametrize("span", [0, 18, 30, 60, 62, 100])
+def test_quantiser_bits_over_the_range_of_scales(kind, span):
+    """60,000 rows of every spread of magnitudes, 2^-span .. 2^span: each quotient by the row's
+    scale rounds as the division does, on both sides of where the quick form is left."""
+    b = _batch(7500, 1, 4, 64, 32, kind, 16, seed=span)
+    pool, rope, q, k, v, seq, pos, bt, rp = b
+    g = torch.Generator(device=DEV).manual_seed(span)
+    e = (torch.rand(7500, 4, 1, generator=g, device=DEV) * 2 - 1) * span
+    k = (k.float() * torch.exp2(e)).to(torch.bfloat16)
+    v = (v.float() * torch.exp2(-e)).to(torch.bfloat16)
+    got = pa_kv_append_rope(pool, rope, q, k, v, seq, pos, bt)
+    _check(pool, rope, q, k, v, seq, pos, bt, rp, got)
+
+
+@gpu
 def test_slices_of_a_fused_projection_and_in_place():
     pool, rope, q, k, v, seq, pos, bt, rp = _batch(53, 8, 2, 128, 16, "bf16", 128)
     qkv = torch.cat([q.flatten(1), k.flatten(1), v.flatten(1)], 1).contiguous()
