@@ -718,8 +718,9 @@ pa_status_t check_prefill(const pa_kv_pool_t *pool, int n, int B, int hq, int ma
   if (hq / pool->num_kv_heads > kMaxGroup)
     return fail(PA_ERR_UNSUPPORTED, "GQA group %d > %d query heads per KV head",
                 hq / pool->num_kv_heads, kMaxGroup);
-  if (n > (1 << 24) || B > 65535 || hq > 65535)
-    return fail(PA_ERR_UNSUPPORTED, "at most 2^24 tokens, 65535 sequences and 65535 heads");
+  if (n > (1 << 24) || B > 65535 || hq > 65535 || (long long)n * hq > (1LL << 31))
+    return fail(PA_ERR_UNSUPPORTED,
+                "at most 2^24 tokens, 65535 sequences, 65535 heads and 2^31 query rows");
   if ((long long)max_pages * pool->page_size > (1LL << 30))
     return fail(PA_ERR_UNSUPPORTED, "max_pages * page_size too large");
   return PA_OK;

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
   const int b = c.seq, qlen = c.qlen, ctx = c.ctx;
   const int rows = qlen * G - c.blk * kCtaRows;  // of this CTA; may pass 256
 
-  // ---- this thread's row: what it sees, its query into shared memory
+  // ---- this thread's row: what it sees
   int lo = 0, hi = 0x7fffffff;  // an unused row masks nothing
   int pos = 0;
   bool row_ok = false;
@@ -414,22 +414,6 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       if (a.doc_begin != nullptr) lo = max(__ldg(a.doc_begin + c.q0 + tok), 0);
       if (hi <= lo) lo = hi = 0;
     }
-    // the warp's 32 query rows, D / 8 lanes a row (rows past the last: zeros)
-    const uint32_t dst = sbase + L::kQOff + sub * L::kQBytes;
-    constexpr int kRowLanes = D / 8;
-#pragma unroll
-    for (int i = 0; i < kRowLanes; ++i) {
-      const int r = i * (32 / kRowLanes) + lane / kRowLanes, k = lane % kRowLanes;
-      const size_t from = __shfl_sync(0xffffffffu, (unsigned long long)orow, r);
-      const bool live = __shfl_sync(0xffffffffu, (int)row_ok, r) != 0;
-      const unsigned char *src = static_cast<const unsigned char *>(a.q) + from * D * 2 + k * 16;
-      const uint32_t to = dst + sw128((warp & 3) * 32 + r, k, kTile);
-      if constexpr (kQuant)
-        sts_u4(to, place8<KVT>(live ? ldg_nc128(src) : make_uint4(0, 0, 0, 0)));
-      else
-        cp_async16(to, src, live ? 16u : 0u);
-    }
-    cp_async_commit();
     const bool sees = row_ok && hi > lo;
     const int wlo = __reduce_min_sync(0xffffffffu, sees ? lo : 0x7fffffff);
     const int whi = __reduce_max_sync(0xffffffffu, sees ? hi : 0);
@@ -445,7 +429,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
-  __syncthreads();  // the key range and the TMEM address; the queries are still on their way
+  __syncthreads();  // the key range and the TMEM address: the loads may begin
   tc_fence_after();
 
   // ---- this split's key tiles [t0, t1), walked from t1 - 1 down
@@ -671,6 +655,24 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<KVT>));
+    // the warp's 32 query rows, D / 8 lanes a row (rows past the last: zeros)
+    const uint32_t dst = sbase + L::kQOff + sub * L::kQBytes;
+    constexpr int kRowLanes = D / 8;
+    if (sub < subs) {  // (else its place belongs to the loaders)
+#pragma unroll
+      for (int i = 0; i < kRowLanes; ++i) {
+        const int r = i * (32 / kRowLanes) + lane / kRowLanes, k = lane % kRowLanes;
+        const size_t from = __shfl_sync(0xffffffffu, (unsigned long long)orow, r);
+        const bool live = __shfl_sync(0xffffffffu, (int)row_ok, r) != 0;
+        const unsigned char *src = static_cast<const unsigned char *>(a.q) + from * D * 2 + k * 16;
+        const uint32_t to = dst + sw128((warp & 3) * 32 + r, k, kTile);
+        if constexpr (kQuant)
+          sts_u4(to, place8<KVT>(live ? ldg_nc128(src) : make_uint4(0, 0, 0, 0)));
+        else
+          cp_async16(to, src, live ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
     cp_async_wait<0>();
     proxy_fence();
     bar_arrive(smem_u32(&c.q_full));
@@ -834,16 +836,31 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
           if (!quick) tmem_wait_st();  // this P is written over
         }
         if (!quick) {
+          if constexpr (MODE == 0) {
+            const f32x2 mul_2 = pack2(mul, mul);
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) {
-            s[j] *= mul;
-            if constexpr (kCap) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
-            if constexpr (kBias) s[j] -= slope * fabsf((float)(pos - k0 - j));
+            for (int j = 0; j < kKeys; j += 2) unpack2(mul2(pack2(s[j], s[j + 1]), mul_2), s[j], s[j + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+              s[j] *= mul;
+              if constexpr (kCap) s[j] = a.cap_l2 * tanh_f32(s[j] * a.inv_cap);
+              if constexpr (kBias) s[j] -= slope * fabsf((float)(pos - k0 - j));
+            }
           }
           if (!full) {
+            // 32 keys at a time: most such blocks are seen by all the warp's rows
+            // (packed documents 242 -> 239 us; the capped kernel, whose registers
+            // it costs, 562 -> 606 us, does without)
+            const int begin = lo - k0, end = hi - k0;
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if ((unsigned)(k0 + j - lo) >= (unsigned)(hi - lo)) s[j] = -INFINITY;
+            for (int c0 = 0; c0 < kKeys; c0 += 32) {
+              if (MODE == kCapped || !__all_sync(0xffffffffu, begin <= c0 && end >= c0 + 32)) {
+#pragma unroll
+                for (int j = c0; j < c0 + 32; ++j)
+                  if ((unsigned)(j - begin) >= (unsigned)(end - begin)) s[j] = -INFINITY;
+              }
+            }
             if (!all_valid) {
 #pragma unroll
               for (int j = 0; j < kKeys; ++j)

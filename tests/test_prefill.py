@@ -303,6 +303,28 @@ def test_graph_replay_shared_workspace_and_determinism():
     assert torch.equal(a, b)
 
 
+@gpu
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, beside a busy default stream."""
+    cases = []
+    for seed, (qlens, lens, kind) in enumerate([([700, 33], [900, 2000], "bf16"), ([5, 6, 7], [3000, 40, 7], "u8")]):
+        pool, bt, ctx, g = make_batch(lens, 8, 2, 128, 16, kind, seed=seed)
+        q, begin, n = _queries(g, qlens, 8, 128)
+        ws = torch.zeros(1 << 25, dtype=torch.uint8, device=DEV)
+        cases.append((pool, q, begin, bt, ctx, n, ws, torch.full_like(q, 7.0),
+                      torch.full(q.shape[:2], 7.0, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device=DEV)
+    for _ in range(4):
+        busy = busy @ busy * 1e-3
+        for pool, q, begin, bt, ctx, n, ws, out, lse, stream in cases:
+            pa_prefill(pool, q, begin, bt, ctx, 0.09, softcap=20.0, out=out, lse_out=lse, workspace=ws,
+                       num_splits=3, stream=stream)
+    torch.cuda.synchronize()
+    for pool, q, begin, bt, ctx, n, ws, out, lse, stream in cases:
+        _check(pool, q, begin, bt, ctx, 0.09, n, out, lse, softcap=20.0)
+
+
 # ---- refusals, without a GPU -------------------------------------------------------
 
 
@@ -338,6 +360,7 @@ def test_refusals(lib):
     assert _call(lib, hq=18) == PA_ERR_UNSUPPORTED
     assert _call(lib, n=-1) == PA_ERR_INVALID_ARG
     assert _call(lib, n=(1 << 24) + 1) == PA_ERR_UNSUPPORTED
+    assert _call(lib, pool=_pool(num_kv_heads=32), n=1 << 24, hq=256) == PA_ERR_UNSUPPORTED
     assert _call(lib, max_pages=0) == PA_ERR_INVALID_ARG
     assert _call(lib, splits=-1) == PA_ERR_INVALID_ARG
     assert _call(lib, scale=float("nan")) == PA_ERR_INVALID_ARG
