@@ -50,8 +50,10 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
                     pack_bf16(x[6], x[7]));
 }
 
+// (Quantised pools: six CTAs per SM, 80 registers, 70.6 -> 67.7 us for 8,000
+// image tokens of 64/8 heads into an FP8 cache; bf16 pools lose by it.)
 template <int D, int KVT, bool IL>
-__global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendRopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, KVT == PA_KV_BF16 ? 0 : 6) append_rope_kernel(const AppendRopeArgs a) {
   pdl_launch_dependents();
   pdl_wait_primary();
   constexpr int kLanes = D / 16;         // lanes of one row
@@ -225,7 +227,10 @@ cudaError_t launch_t(const AppendRopeArgs &a, bool interleaved, cudaStream_t str
   const long long items =
       (long long)a.n * ((a.hq + 2 * a.hkv + item_rows - 1) / item_rows);
   const long long want = (items + kWarps - 1) / kWarps;
-  const long long most = 32LL * device_sm_count();
+  // a few items per warp even out the costly key and value rows (8,000 tokens,
+  // FP8: 16 CTAs per SM 69.0 us, 32 70.6, one item per warp 75.6; at 5 per SM
+  // the same warps get those rows every time, 96.8)
+  const long long most = 16LL * device_sm_count();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(want < most ? want : most));
   cfg.blockDim = dim3(kWarps * 32);
