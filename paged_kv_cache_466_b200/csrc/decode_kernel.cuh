@@ -244,8 +244,10 @@ struct ScoreMod {
   __device__ __forceinline__ float cap(float x) const {
     return cap_l2 * tanh_f32(x * inv_cap);
   }
-  __device__ __forceinline__ float bias(int tok, int i) const {
-    return slope[i] * static_cast<float>(pos - tok);
+  // x with the bias of the key `off` tokens after the one that `dist` is the
+  // distance of (one conversion of a distance per block, not per score)
+  __device__ __forceinline__ float biased(float x, float dist, int off, int i) const {
+    return fmaf(-slope[i], dist - static_cast<float>(off), x);
   }
 };
 
@@ -510,13 +512,15 @@ __device__ __forceinline__ void block_step(const LaneMap<D, PA_KV_BF16> &lm, uin
   // ---- online softmax (log2 domain) ---------------------------------------
   float x[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};  // tokens 2t, 2t+1, 8+2t, 9+2t
   if constexpr (MOD) {
+    const float dist = static_cast<float>(mod.pos - btok - 2 * t);
+    const bool whole = pvalid && btok >= tok_lo && btok + 16 <= tok1;  // warp-uniform
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int tok = btok + (e & 1) + 2 * t + (e >> 1) * 8;
-      const bool ok = pvalid && tok >= tok_lo && tok < tok1;
+      const int off = (e & 1) + (e >> 1) * 8, tok = btok + 2 * t + off;
       x[e] *= scale_log2;
       if (mod.cap_l2 > 0.f) x[e] = mod.cap(x[e]);
-      x[e] = ok ? x[e] - mod.bias(tok, 0) : -INFINITY;
+      x[e] = mod.biased(x[e], dist, off, 0);
+      if (!whole && !(pvalid && tok >= tok_lo && tok < tok1)) x[e] = -INFINITY;
     }
   } else if (pvalid && btok >= tok_lo && btok + 16 <= tok1) {  // warp-uniform: no mask needed
 #pragma unroll
@@ -850,8 +854,9 @@ __device__ __forceinline__ void pair_step(const LaneMap<D, KVT> &lm, uint32_t sr
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[u][e] = mod.cap(x[u][e]);
       }
+      const float dist = static_cast<float>(mod.pos - btok[u] - g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[u][e] -= mod.bias(btok[u] + g + 8 * (e >> 1), e & 1);
+      for (int e = 0; e < 4; ++e) x[u][e] = mod.biased(x[u][e], dist, 8 * (e >> 1), e & 1);
     }
     vs[u][0] = __uint_as_float(v0.x);
     vz[u][0] = __uint_as_float(v0.y);

@@ -31,6 +31,18 @@
 //
 // P is rounded to bf16 (half a step, 2^-9 of each weight's binade) as the
 // output is; the denominator and all statistics stay fp32.
+//
+// What bounds it: the chain of one row tile. A tile of 256 rows and 128 keys
+// takes 3180 clocks: softmax 1720 (128 exponentials a thread are 1024 clocks of
+// the special-function unit), hand-over 140, PV and S 1024, their completion
+// 290; the MMAs of both row tiles fill 2048 of them. Around the tiles a CTA
+// spends about 10,000 clocks (finding its rows, first loads, output).
+// Measured on B200, 32/8 heads of 128, one prompt of 8192 bf16 tokens, causal:
+// 450 us, 1220 TFLOP/s (75 % of the measured library rate), capped 560 us.
+// Tried and slower: two threads per row (535 against 494 us then), 64-key tiles
+// with the next scores computed early (765; an N of 64 reads A from shared
+// memory twice as often), P handed over in halves (471 against 452), a quarter
+// of the exponentials on the FMA pipe (492 against 474).
 #include <atomic>
 #include <cmath>
 #include <cstddef>
@@ -45,7 +57,7 @@ namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.0f;   // raise the running max only past this
-constexpr float kQuickMost = 1048576.f;  // largest weight sum of a tile done without a maximum
+constexpr float kQuickMost = 1048576.f;  // largest weight sum of a tile done without a maximum pass
 constexpr int kTile = 128;            // query rows of a tile (the MMA's M)
 constexpr int kKeys = 128;            // keys of a tile
 constexpr int kCtaRows = 2 * kTile;
