@@ -454,6 +454,10 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     if (t1 < t0) t1 = t0;
   }
   const int n = t1 - t0;
+  // Of the first tile, blocks (bf16 pools: pages) that end at or before this key
+  // are not read and their table entries not looked at: the cache may have
+  // dropped the pages before the first document.
+  const int first = c.lo;
   const int subs = rows > kTile ? 2 : 1;  // row tiles in use
   const uint32_t tmem = c.tmem;
   volatile int32_t *dead = &c.dead;
@@ -470,7 +474,9 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     const int total = n * 2 * (kKeys / 16);
     const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
     auto token_of = [&](int m) { return (t1 - 1 - (m >> 4)) * kKeys + (m & 7) * 16; };
-    auto there = [&](int m) { return m < total && token_of(m) < ctx; };
+    auto there = [&](int m) {
+      return m < total && token_of(m) < ctx && token_of(m) + 16 > first;
+    };
     // the table's entry for block m, not looked at yet (the load is waited
     // for where it is used, a block later)
     auto entry_of = [&](int m) { return there(m) ? __ldg(table + (token_of(m) >> p_log2)) : 0; };
@@ -601,19 +607,21 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
         const int per_tile = kKeys / a.P;
         const uint32_t box = (uint32_t)a.P * 128;
         const int32_t *table = a.block_tables + (size_t)b * a.max_pages;
-        // lane x: the id of page x of tile k; past the context -1
+        // lane x: the id of page x of tile k; past the context or before the
+        // first key -1
+        auto outside = [&](int tok) { return tok >= ctx || tok + a.P <= first; };
         auto page_of = [&](int k) {
           const int tok = (t1 - 1 - k) * kKeys + lane * a.P;
-          return k < n && lane < per_tile && tok < ctx ? __ldg(table + tok / a.P) : -1;
+          return k < n && lane < per_tile && !outside(tok) ? __ldg(table + tok / a.P) : -1;
         };
         int id = page_of(0);
         bool ok = true;
         for (int k = 0; k < n; ++k) {
           const int tile = t1 - 1 - k;
           const int next = page_of(k + 1);
-          const bool past = tile * kKeys + lane * a.P >= ctx;
-          const bool bad = lane < per_tile && !past && (id < 0 || id >= a.num_pages);
-          const int page = past || bad ? a.num_pages : id;  // past the pool: zeros
+          const bool none = outside(tile * kKeys + lane * a.P);
+          const bool bad = lane < per_tile && !none && (id < 0 || id >= a.num_pages);
+          const int page = none || bad ? a.num_pages : id;  // past the pool: zeros
           if (!is_v && lane < per_tile) {
             if (bad) flag_error(a.d_err, PA_DERR_BAD_PAGE);
             for (int x = 0; x < a.P / 16; ++x) c.valid[k % L::kRing][lane * (a.P / 16) + x] = !bad;

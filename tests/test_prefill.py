@@ -199,6 +199,36 @@ def test_bad_pages_lengths_and_rows(kind, splits):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8", "fp8", "u4"])
+@pytest.mark.parametrize("D,P,splits", [(128, 16, 1), (128, 32, 3), (64, 32, 1)])
+def test_pages_before_the_first_document_may_be_dropped(kind, D, P, splits):
+    """Pages that end before the first key any query sees: entries outside the pool, or pages
+    that hold NaN by now. Neither is read; the results are those of the whole table, bit for bit."""
+    lens, firsts, qlens = [700, 333, 129, 520], [333, 200, 128, 256], [90, 40, 1, 200]
+    pool, bt, ctx, g = make_batch(lens, 4, 2, D, P, kind)
+    q, begin, n = _queries(g, qlens, 4, D)
+    doc = torch.cat([torch.full((m,), f, dtype=torch.int32) for m, f in zip(qlens, firsts)]).to(DEV)
+    doc[80:90] = 690                                         # a second document
+    got, lse = _run(pool, q, begin, bt, ctx, 0.1, {"doc_begin": doc}, num_splits=splits)
+    _check(pool, q, begin, bt, ctx, 0.1, n, got, lse, doc_begin=doc)
+    last = torch.tensor([90, 130, 131, 331], device=DEV) - 1
+    step = pa_decode_scored(pool, q[last], bt, ctx, 0.1, doc_begin=doc[last], num_splits=splits)
+    dropped = bt.clone()
+    for b, f in enumerate(firsts):
+        gone = bt[b, :f // P].long()
+        for t in pool.tensors():
+            t[gone] = float("nan") if t.is_floating_point() else 0xFF
+        dropped[b, :f // P:2] = -1
+        dropped[b, 1:f // P:4] = pool.num_pages
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got2, lse2 = _run(pool, q, begin, dropped, ctx, 0.1, {"doc_begin": doc}, num_splits=splits, d_err=err)
+    assert int(err.item()) == 0 and torch.equal(got, got2) and torch.equal(lse, lse2)
+    step2 = pa_decode_scored(pool, q[last], dropped, ctx, 0.1, doc_begin=doc[last], num_splits=splits,
+                             d_err=err)
+    assert int(err.item()) == 0 and torch.equal(step, step2)
+
+
+@gpu
 def test_garbage_behind_the_context_is_not_read():
     """Rows behind the context in its last page, and pages behind it, hold NaN."""
     pool = KVPool(4, 1, 16, 128, "bf16", DEV, fill_byte=0xFF)
