@@ -421,7 +421,8 @@ pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
  *   q_begin  : (device) int32 [num_seqs + 1], ascending, within [0, num_tokens]:
  *              sequence b's query tokens are rows q_begin[b] .. q_begin[b + 1] - 1
  *              (none is allowed); a sequence whose entries are not so is
- *              clamped into range and flagged PA_DERR_BAD_SEQ
+ *              clamped into range and flagged PA_DERR_BAD_SEQ (query rows that
+ *              two sequences of such a call claim then hold anything)
  *   context_lens : (device) int32 [num_seqs]; one that is below the sequence's
  *              query tokens or past its table flags PA_DERR_BAD_CTX and its
  *              queries see nothing (out = 0)

@@ -1011,9 +1011,17 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a)
   pdl_wait_primary();
   const int lane = threadIdx.x & 31;
   const size_t row = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int first = max(__ldg(a.q_begin), 0), last = min(__ldg(a.q_begin + a.B), a.n);
-  // rows outside the sequences are left as they were
-  if (row >= (size_t)last * a.hq || row < (size_t)first * a.hq) return;
+  if (row >= (size_t)a.n * a.hq) return;  // (the grid is rounded up to whole CTAs)
+  // Rows outside the sequences, clamped as prefill_kernel clamps them, have no
+  // partials and are left as they were.
+  const int tok = (int)(row / a.hq);
+  bool mine = false;
+  for (int b0 = 0; b0 < a.B && !mine; b0 += 32) {
+    const int b = b0 + lane;
+    mine = __any_sync(0xffffffffu, b < a.B && tok >= max(__ldg(a.q_begin + min(b, a.B)), 0) &&
+                                       tok < min(__ldg(a.q_begin + min(b + 1, a.B)), a.n));
+  }
+  if (!mine) return;
   const float *lse = a.lse_part + row * a.S;
   float M = -INFINITY;
   for (int s = lane; s < a.S; s += 32) M = fmaxf(M, __ldcg(lse + s));

@@ -1,0 +1,61 @@
+"""The edges of the rotating cache write, prompt attention and scored decode:
+malformed batches, queries that are not numbers, rows that see nothing, caps and
+scales at the ends of their range, storage that a call allocates. The 64-bit
+definitions and the tolerances are those of test_prefill.py and
+test_decode_scored.py."""
+import pytest
+import torch
+
+from paged_kv_cache_466_b200 import PA_DERR_BAD_SEQ, pa_prefill
+from tests.helpers import DEV
+from tests.scored_ref import make_batch
+from tests.test_prefill import _queries
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8"])
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("entries,whole", [
+    ({3: -5}, [(0, 40)]),                 # the last entry negative
+    ({3: 17}, [(0, 23), (23, 40)]),       # the last sequence descends into the others' rows
+    ({2: 3}, [(0, 23)]),                  # an interior entry descends
+    ({0: -7, 3: 10 ** 9}, [(23, 40)]),    # both ends out of range
+    ({0: 2 ** 31 - 1}, [(23, 40), (40, 41)]),
+])
+def test_malformed_query_ranges_stay_inside_the_outputs(kind, splits, entries, whole):
+    """No row outside the outputs is written (41 x 6 rows: the last CTA of a merge is not full),
+    the call is flagged, and sequences whose own entries are in order, and whose rows no other
+    sequence claims, keep their results bit for bit."""
+    qlens, lens, Hq = [23, 17, 1], [900, 700, 300], 6
+    pool, bt, ctx, g = make_batch(lens, Hq, 2, 128, 16, kind)
+    q, begin, n = _queries(g, qlens, Hq, 128)
+    q = q[:n].contiguous()
+    bad = begin.clone()
+    for i, x in entries.items():
+        bad[i] = x
+
+    def run(b, err):
+        out = torch.full((n * Hq + 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((n * Hq + 8,), 7.0, device=DEV)
+        pa_prefill(pool, q, b, bt, ctx, 0.1, out=out[:n * Hq].view(n, Hq, 128),
+                   lse_out=lse[:n * Hq].view(n, Hq), num_splits=splits, d_err=err)
+        assert torch.all(out[n * Hq:] == 7.0) and torch.all(lse[n * Hq:] == 7.0)
+        return out[:n * Hq].view(n, Hq, 128), lse[:n * Hq].view(n, Hq)
+
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    good, glse = run(begin, err)
+    assert int(err.item()) == 0 and not torch.any(good == 7.0)
+    out, lse = run(bad, err)
+    assert int(err.item()) & PA_DERR_BAD_SEQ
+    b = [min(max(int(x), 0), n) for x in bad.tolist()]
+    claimed = torch.zeros(n, dtype=torch.int32)
+    for s, e in zip(b, b[1:]):
+        claimed[s:max(e, s)] += 1
+    for s, e in whole:
+        for i in range(s, e):
+            if claimed[i] == 1:
+                assert torch.equal(out[i], good[i]) and torch.equal(lse[i], glse[i])
+    idle = (claimed == 0).to(DEV)
+    assert torch.all(out[idle] == 7.0) and torch.all(lse[idle] == 7.0)
