@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       const int q0 = __ldg(a.q_begin + b), q1 = __ldg(a.q_begin + b + 1);
       ctx = __ldg(a.ctx + b);
       s = max(q0, 0);
-      len = max(min(q1, a.n) - s, 0);
+      len = max(min(q1, a.n), s) - s;  // (no entry makes the difference wrap)
       if (blockIdx.x == 0 && (q0 < 0 || q1 > a.n || q1 < q0)) flag_error(a.d_err, PA_DERR_BAD_SEQ);
       nb = (int)(((long long)len * G + kCtaRows - 1) / kCtaRows);
     };

@@ -19,6 +19,7 @@ gpu = pytest.mark.gpu
 @pytest.mark.parametrize("splits", [1, 3])
 @pytest.mark.parametrize("entries,whole", [
     ({3: -5}, [(0, 40)]),                 # the last entry negative
+    ({3: -2 ** 31}, [(0, 40)]),
     ({3: 17}, [(0, 23), (23, 40)]),       # the last sequence descends into the others' rows
     ({2: 3}, [(0, 23)]),                  # an interior entry descends
     ({0: -7, 3: 10 ** 9}, [(23, 40)]),    # both ends out of range
