@@ -678,7 +678,10 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
     // the warp's 32 query rows, D / 8 lanes a row (rows past the last: zeros)
     const uint32_t dst = sbase + L::kQOff + sub * L::kQBytes;
     constexpr int kRowLanes = D / 8;
-    if (sub < subs) {  // (else its place belongs to the loaders)
+    // (a second row tile that is not used leaves its place to the loaders;
+    // without a key tile nothing waits for the queries of the other warps, which
+    // the rows staged below would meet in shared memory)
+    if (sub < subs && n > 0) {
 #pragma unroll
       for (int i = 0; i < kRowLanes; ++i) {
         const int r = i * (32 / kRowLanes) + lane / kRowLanes, k = lane % kRowLanes;

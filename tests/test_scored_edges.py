@@ -9,7 +9,7 @@ import torch
 from paged_kv_cache_466_b200 import PA_DERR_BAD_SEQ, pa_prefill
 from tests.helpers import DEV
 from tests.scored_ref import make_batch
-from tests.test_prefill import _queries
+from tests.test_prefill import _check, _queries, _run
 
 gpu = pytest.mark.gpu
 
@@ -60,3 +60,21 @@ def test_malformed_query_ranges_stay_inside_the_outputs(kind, splits, entries, w
                 assert torch.equal(out[i], good[i]) and torch.equal(lse[i], glse[i])
     idle = (claimed == 0).to(DEV)
     assert torch.all(out[idle] == 7.0) and torch.all(lse[idle] == 7.0)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8", "u4"])
+@pytest.mark.parametrize("D,P", [(128, 16), (64, 32)])
+def test_blocks_whose_rows_all_see_nothing(kind, D, P):
+    """Blocks of 256 rows without a single key: their zeros go out through shared memory that no
+    query may still be on its way to. Many blocks, several times; queries far from zero."""
+    qlens, lens, Hq = [1500, 200, 900], [1600, 333, 900], 8
+    pool, bt, ctx, g = make_batch(lens, Hq, 2, D, P, kind)
+    q, begin, n = _queries(g, qlens, Hq, D, 100.0)
+    pos = torch.cat([torch.arange(c - m, c) for m, c in zip(qlens, lens)]).to(DEV)
+    blind = (torch.arange(n, device=DEV) < 1500) | (torch.arange(n, device=DEV) >= 1700)
+    doc = torch.where(blind, pos + 1, 0).to(torch.int32)
+    for _ in range(10):
+        got, lse = _run(pool, q, begin, bt, ctx, 1e-3, {"doc_begin": doc}, num_splits=1)
+        assert torch.all(got[:n][blind] == 0) and torch.all(lse[:n][blind] == -float("inf"))
+    _check(pool, q, begin, bt, ctx, 1e-3, n, got, lse, doc_begin=doc)
