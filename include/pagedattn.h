@@ -366,7 +366,8 @@ pa_status_t pa_decode_append(const pa_kv_pool_t *pool, const void *q,
  *                  cache positions of the query's token and of the key
  * and key j takes part for query i only if
  *   doc_begin_i <= j  and  (j <= i or j < prefix_end_i)  and  j < context length.
- * A query that sees no key gets out = 0. Pages before the one that holds the
+ * A query that sees no key gets out = 0; one that has a NaN score gets NaN,
+ * however the keys are split. Pages before the one that holds the
  * first key any query of their sequence sees are not read, nor their table
  * entries looked at: they may be dropped. From that page on all keys and values
  * of the context must be finite, also those that are masked.

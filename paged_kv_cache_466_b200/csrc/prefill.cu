@@ -1033,21 +1033,22 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a)
   constexpr int E = D / 32;
   float acc[E] = {};
   float den = 0.f;
-  if (M > -INFINITY) {
-    for (int s = 0; s < a.S; ++s) {
-      const float w = expf(__ldcg(lse + s) - M);
-      if (w == 0.f) continue;
-      den += w;
-      const float *o = a.o_part + (row * a.S + s) * D + lane * E;
+  for (int s = 0; s < a.S; ++s) {
+    // (the maximum drops NaN; a partial that is NaN keeps a NaN weight, so the
+    // row is NaN however its keys are split)
+    const float l = __ldcg(lse + s);
+    const float w = l == -INFINITY ? 0.f : expf(l - M);
+    if (w == 0.f) continue;
+    den += w;
+    const float *o = a.o_part + (row * a.S + s) * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __ldcg(o + e), acc[e]);
-    }
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, __ldcg(o + e), acc[e]);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (a.lse_out != nullptr && lane == 0) a.lse_out[row] = den > 0.f ? M + logf(den) : -INFINITY;
+  if (a.lse_out != nullptr && lane == 0) a.lse_out[row] = den == 0.f ? -INFINITY : M + logf(den);
 }
 
 bool encode_pool(CUtensorMap *map, const void *pool, int D, int P, int hkv, int num_pages) {

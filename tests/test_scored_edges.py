@@ -78,3 +78,24 @@ def test_blocks_whose_rows_all_see_nothing(kind, D, P):
         got, lse = _run(pool, q, begin, bt, ctx, 1e-3, {"doc_begin": doc}, num_splits=1)
         assert torch.all(got[:n][blind] == 0) and torch.all(lse[:n][blind] == -float("inf"))
     _check(pool, q, begin, bt, ctx, 1e-3, n, got, lse, doc_begin=doc)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8", "fp8", "u4"])
+@pytest.mark.parametrize("splits", [1, 3, 0])
+def test_a_query_that_is_not_a_number_gives_nan(kind, splits):
+    """NaN in one head, in all heads of a token, an infinity: out and lse of those rows are NaN
+    however the keys are split, and the others hold their result."""
+    qlens, lens = [40, 3], [1500, 700]
+    pool, bt, ctx, g = make_batch(lens, 6, 2, 128, 16, kind)
+    q, begin, n = _queries(g, qlens, 6, 128)
+    sick = torch.zeros(n, 6, dtype=torch.bool, device=DEV)
+    sick[5, 1] = sick[41] = sick[17, 4] = True
+    bad = q.clone()
+    bad[5, 1, 7] = bad[41] = float("nan")
+    bad[17, 4, 3] = float("inf")
+    clean, clse = _run(pool, q, begin, bt, ctx, 0.1, {}, num_splits=splits)
+    got, lse = _run(pool, bad, begin, bt, ctx, 0.1, {}, num_splits=splits)
+    assert torch.isnan(got[:n][sick]).all() and torch.isnan(lse[:n][sick]).all()
+    got[:n][sick], lse[:n][sick] = clean[:n][sick], clse[:n][sick]
+    _check(pool, q, begin, bt, ctx, 0.1, n, got, lse)
