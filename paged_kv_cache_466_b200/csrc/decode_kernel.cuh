@@ -173,8 +173,9 @@ __device__ __forceinline__ int out_col(int j, int g) {
 // nl partials of this call's splits (workspace slots 0..nl-1) plus the
 // caller's prior partials (e.g. a shared prefix), in that fixed order. Every
 // thread of the CTA must call it; `wts` is shared scratch of
-// G * (nl + n_prior) floats. Writes out[b][h*G + hd][:].
-template <int D>
+// G * (nl + n_prior) floats. Writes out[b][h*G + hd][:]. The maximum drops NaN:
+// with kNan a partial that is NaN keeps a NaN weight, so its row is NaN.
+template <int D, bool kNan>
 __device__ void merge_rows(const DecodeArgs &a, int b, int h, int G, int nl, float *wts) {
   const int nw = nl + a.n_prior;
   const size_t R = (size_t)a.B * a.hq;
@@ -192,7 +193,8 @@ __device__ void merge_rows(const DecodeArgs &a, int b, int h, int G, int nl, flo
     for (int sp = 0; sp < nw; ++sp) M = fmaxf(M, wh[sp]);
     float den = 0.f;
     for (int sp = 0; sp < nw; ++sp) {
-      const float wv = M == -INFINITY ? 0.f : expf(wh[sp] - M);
+      const bool none = kNan ? wh[sp] == -INFINITY : M == -INFINITY;
+      const float wv = none ? 0.f : expf(wh[sp] - M);
       wh[sp] = wv;
       den += wv;
     }
@@ -1210,7 +1212,7 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
         }
       }
       if (a.n_prior > 0) {  // nothing of our own: the output is the priors' merge
-        merge_rows<D>(a, b, h, G, 0, reinterpret_cast<float *>(smem));
+        merge_rows<D, MOD>(a, b, h, G, 0, reinterpret_cast<float *>(smem));
       } else {  // empty context: the output is 0
         for (int e = threadIdx.x; e < G * D; e += W * 32)
           a.out[((size_t)b * a.hq + (size_t)h * G) * D + e] = 0.f;
@@ -1483,6 +1485,12 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
         num.w = fmaf(fl, v.w, num.w);
         L += fl;
       }
+    } else if constexpr (MOD) {
+      // no key seen, or a NaN score in every key's place (fmaxf dropped it): 0 or NaN
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        L += reinterpret_cast<const float *>(smem + w * SM::kRingBytesPerWarp)[8 + hd];
+      num = make_float4(L, L, L, L);
     }
     const size_t row = (size_t)b * a.hq + (size_t)h * G + hd;
     const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -1491,14 +1499,15 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
       reinterpret_cast<float4 *>(a.out + row * D)[d4] = val;
     } else {
       reinterpret_cast<float4 *>(a.o_part + (row * a.S + slot) * D)[d4] = val;
-      if (d4 == 0) a.lse[row * a.S + slot] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+      const bool some = MOD ? L != 0.f : L > 0.f;  // (true for NaN with MOD)
+      if (d4 == 0) a.lse[row * a.S + slot] = some ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
   }
   if (a.keep_partials) return;  // the caller merges
   if (n_live == 1) {
     if (a.n_prior == 0) return;
     __syncthreads();  // our own partial is visible to the whole CTA
-    merge_rows<D>(a, b, h, G, 1, reinterpret_cast<float *>(smem));
+    merge_rows<D, MOD>(a, b, h, G, 1, reinterpret_cast<float *>(smem));
     return;
   }
 
@@ -1516,7 +1525,7 @@ __global__ void __launch_bounds__(W * 32, kMinCtas<KVT>) decode_kernel(const Ker
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  merge_rows<D>(a, b, h, G, n_live, reinterpret_cast<float *>(smem));
+  merge_rows<D, MOD>(a, b, h, G, n_live, reinterpret_cast<float *>(smem));
   if (threadIdx.x == 0) a.counters[(size_t)b * a.hkv + h] = 0;
 }
 

@@ -6,9 +6,10 @@ test_decode_scored.py."""
 import pytest
 import torch
 
-from paged_kv_cache_466_b200 import PA_DERR_BAD_SEQ, pa_prefill
+from paged_kv_cache_466_b200 import PA_DERR_BAD_SEQ, pa_decode_scored, pa_prefill
 from tests.helpers import DEV
 from tests.scored_ref import make_batch
+from tests.test_decode_scored import _check as _check_step
 from tests.test_prefill import _check, _queries, _run
 
 gpu = pytest.mark.gpu
@@ -99,3 +100,25 @@ def test_a_query_that_is_not_a_number_gives_nan(kind, splits):
     assert torch.isnan(got[:n][sick]).all() and torch.isnan(lse[:n][sick]).all()
     got[:n][sick], lse[:n][sick] = clean[:n][sick], clse[:n][sick]
     _check(pool, q, begin, bt, ctx, 0.1, n, got, lse)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8", "fp8", "u4"])
+@pytest.mark.parametrize("G", [3, 8])
+def test_a_step_whose_query_is_not_a_number_gives_nan(kind, G):
+    lens = [1500, 700, 1, 400]
+    pool, bt, ctx, g = make_batch(lens, 2 * G, 2, 128, 16, kind)
+    q = torch.randn(4, 2 * G, 128, generator=g, device=DEV).to(torch.bfloat16)
+    sick = torch.zeros(4, 2 * G, dtype=torch.bool, device=DEV)
+    sick[0, 1] = sick[1] = sick[2, 4] = True
+    bad = q.clone()
+    bad[0, 1, 7] = bad[1] = bad[2, 4, 3] = float("nan")
+    doc = torch.tensor([0, 0, 0, 400], dtype=torch.int32, device=DEV)   # the last sees nothing
+    bad[3] = float("nan")
+    for splits in (1, 3):
+        kw = dict(softcap=9.0, doc_begin=doc)
+        clean = pa_decode_scored(pool, q, bt, ctx, 0.1, num_splits=splits, **kw)
+        got = pa_decode_scored(pool, bad, bt, ctx, 0.1, num_splits=splits, **kw)
+        assert torch.isnan(got[sick]).all() and torch.all(got[3] == 0)
+        got[sick] = clean[sick]
+        _check_step(pool, q, bt, ctx, 0.1, got, **kw)
