@@ -30,6 +30,11 @@ Entry points (same names as the C ABI, see include/pagedattn.h):
                            that cannot allocate device memory (the scratch is
                            a fixed-size array owned by the library)
 
+Every call runs on torch's current stream, or on ``stream``. Its inputs have to be
+ready there, and to live (or be recorded on that stream) until it is done; outputs
+and workspaces that the call allocates itself belong to that stream, and the
+caller's stream waits for it before it reads them.
+
 ``KVPool`` owns the page pool tensors; ``Rope`` describes a rotary position
 embedding; ``pages`` holds the host-side page
 allocator and cache-size formulas.
@@ -92,6 +97,24 @@ def _stream(stream=None):
     if _raw_stream is not None:
         return _raw_stream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _own(shape, dtype, device, stream, zero: bool = False) -> torch.Tensor:
+    """Storage that a call allocates itself: on the stream that it runs on, so that a fill comes
+    before the kernel, and the memory is handed out again only behind it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream) -> torch.Tensor:
+    """The same for an output, which the caller goes on to use on its current stream."""
+    t = _own(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def _need(t: torch.Tensor, name: str, dtype, device=None):
@@ -289,7 +312,7 @@ def pa_kv_append_rope(pool: KVPool, rope: Rope, q: Optional[torch.Tensor], k_new
         hq = q.shape[1] if q.dim() == 3 else 0
         qs = _token_rows(q, "q", hq, D, dev)
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = q.new_empty(q.shape) if stream is None else _result(q.shape, q.dtype, dev, stream)
         else:
             _need(q_out, "q_out", torch.bfloat16, dev)
         if q.shape[0] != n or q_out.shape != q.shape:
@@ -325,14 +348,14 @@ def pa_decode(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
     if D != pool.head_dim or block_tables.shape[0] != B or context_lens.numel() != B:
         raise ValueError("pa_decode: shape mismatch")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _result((B, Hq, D), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     max_pages = block_tables.shape[1]
     if workspace is None:
         S = pa_decode_num_splits(pool, B, max_pages, num_splits)
         need = pa_decode_workspace_bytes(B, Hq, D, S)
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode(ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables),
                                max_pages, _ptr(context_lens), float(scale), _ptr(out),
@@ -366,14 +389,14 @@ def pa_decode_append(pool: KVPool, q: torch.Tensor, k_new: torch.Tensor, v_new: 
             or tuple(k_new.shape) != (B, pool.num_kv_heads, D) or k_new.shape != v_new.shape:
         raise ValueError("pa_decode_append: shape mismatch")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _result((B, Hq, D), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     max_pages = block_tables.shape[1]
     if workspace is None:
         need = pa_decode_workspace_bytes(B, Hq, D,
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if host_context_lens is not None:
         hl = host_context_lens
@@ -449,7 +472,8 @@ def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
             raise ValueError("pa_decode_scored: rope_pos must be [num_axes, sequences] of a rope")
     score = _score(softcap, alibi_slopes, Hq, doc_begin, None, B, dev)
     if out is None:
-        out = q.new_empty((B, Hq, D), dtype=torch.float32)
+        out = (q.new_empty((B, Hq, D), dtype=torch.float32) if stream is None
+               else _result((B, Hq, D), torch.float32, dev, stream))
     else:
         _need(out, "out", torch.float32, dev)
         if out.shape != q.shape:
@@ -459,7 +483,7 @@ def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
         need = pa_decode_workspace_bytes(B, Hq, D,
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode_scored(
         ctypes.byref(pool.c), ctypes.byref(score), None if rope is None else ctypes.byref(rope.c),
@@ -503,7 +527,8 @@ def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_table
         raise ValueError("pa_prefill: shape mismatch")
     score = _score(softcap, alibi_slopes, Hq, doc_begin, prefix_end, N, dev)
     if out is None:
-        out = q.new_empty((N, Hq, D))
+        out = (q.new_empty((N, Hq, D)) if stream is None
+               else _result((N, Hq, D), q.dtype, dev, stream))
     else:
         _need(out, "out", torch.bfloat16, dev)
         if out.shape != q.shape:
@@ -515,7 +540,7 @@ def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_table
     if workspace is None:
         need = pa_prefill_workspace_bytes(pool, N, B, Hq, max_pages, num_splits)
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream)  # (partials: written before they are read)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_prefill(
         ctypes.byref(pool.c), ctypes.byref(score), _ptr(q), N, Hq, _ptr(q_begin), B,
@@ -549,13 +574,13 @@ def pa_decode_shared_prefix(pool: KVPool, q: torch.Tensor, prefix_pages: torch.T
     if D != pool.head_dim or block_tables.shape[0] != B or context_lens.numel() != B:
         raise ValueError("pa_decode_shared_prefix: shape mismatch")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _result((B, Hq, D), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     max_pages = block_tables.shape[1]
     if workspace is None:
         need = pa_decode_shared_prefix_workspace_bytes(pool, B, Hq, max_pages, prefix_len,
                                                        num_splits)
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _own(max(need, 256), torch.uint8, dev, stream, zero=True)
     ws_bytes = workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode_shared_prefix(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(prefix_pages), int(prefix_len),
@@ -587,7 +612,7 @@ def pa_decode_window(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
     if D != pool.head_dim or block_tables.shape[0] != B or context_lens.numel() != B:
         raise ValueError("pa_decode_window: shape mismatch")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _result((B, Hq, D), torch.float32, dev, stream)
     _need(out, "out", torch.float32, dev)
     max_pages = block_tables.shape[1]
     if workspace is None:
@@ -596,7 +621,7 @@ def pa_decode_window(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
                 pa_decode_workspace_bytes(B, Hq, D,
                                           pa_decode_num_splits(pool, B, max_pages, num_splits)))
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode_window(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables), max_pages, _ptr(context_lens),
@@ -670,13 +695,13 @@ def pa_decode_step_host(pool: KVPool, packet: StepPacket, scale: float, out_host
             or not out_host.is_contiguous() or tuple(out_host.shape) != (B, Hq, D):
         raise ValueError("pa_decode_step_host: out_host must be a contiguous host fp32 [B, Hq, D]")
     if out_dev is None:
-        out_dev = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out_dev = _result((B, Hq, D), torch.float32, dev, stream)
     _need(out_dev, "out_dev", torch.float32, dev)
     if workspace is None:
         need = pa_decode_workspace_bytes(B, Hq, D,
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode_step_host(
         ctypes.byref(pool.c), ctypes.c_void_p(packet.host.data_ptr()), _ptr(packet.dev),
@@ -715,6 +740,7 @@ class StepGraph:
                                              pa_decode_num_splits(pool, B, max_pages, num_splits))
             if need > 0:
                 workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+                torch.cuda.current_stream(dev).synchronize()  # a launch may go to any stream
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         # keep every buffer the graph points at alive as long as the graph
         self._keep = (pool, packet, out_host, out_dev, workspace, d_err)
@@ -782,7 +808,7 @@ def pa_splitkv_reduce(o_part: torch.Tensor, lse: torch.Tensor,
     if lse.shape != (B, Hq, S):
         raise ValueError("pa_splitkv_reduce: shape mismatch")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=o_part.device)
+        out = _result((B, Hq, D), torch.float32, o_part.device, stream)
     _need(out, "out", torch.float32, o_part.device)
     st = _lib.load().pa_splitkv_reduce(_ptr(o_part), _ptr(lse), B, Hq, S, D, _ptr(out),
                                        _stream(stream))
@@ -812,9 +838,9 @@ def pa_decode_range(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
     if D != pool.head_dim or block_tables.shape[0] != B or context_lens.numel() != B:
         raise ValueError("pa_decode_range: shape mismatch")
     if o_out is None:
-        o_out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        o_out = _result((B, Hq, D), torch.float32, dev, stream)
     if lse_out is None:
-        lse_out = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse_out = _result((B, Hq), torch.float32, dev, stream)
     _need(o_out, "o_out", torch.float32, dev)
     _need(lse_out, "lse_out", torch.float32, dev)
     if tuple(o_out.shape) != (B, Hq, D) or tuple(lse_out.shape) != (B, Hq):
@@ -824,7 +850,7 @@ def pa_decode_range(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
         need = pa_decode_range_workspace_bytes(pool, B, Hq, max_pages, tok_begin, tok_end,
                                                num_splits)
         if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            workspace = _own(need, torch.uint8, dev, stream, zero=True)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.load().pa_decode_range(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables), max_pages, _ptr(context_lens),
@@ -853,9 +879,9 @@ def pa_merge_partials(o_parts: torch.Tensor, lse_parts: torch.Tensor,
     if lse_parts.shape[0] != n or o_parts[0].numel() != rows * D:
         raise ValueError("pa_merge_partials: shape mismatch")
     if out is None:
-        out = torch.empty(o_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
+        out = _result(o_parts.shape[1:], torch.float32, o_parts.device, stream)
     if lse_out is None:
-        lse_out = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
+        lse_out = _result(lse_parts.shape[1:], torch.float32, o_parts.device, stream)
     _need(out, "out", torch.float32, o_parts.device)
     _need(lse_out, "lse_out", torch.float32, o_parts.device)
     st = _lib.load().pa_merge_partials(_ptr(o_parts), _ptr(lse_parts), n, rows, D,

@@ -3,10 +3,15 @@ malformed batches, queries that are not numbers, rows that see nothing, caps and
 scales at the ends of their range, storage that a call allocates. The 64-bit
 definitions and the tolerances are those of test_prefill.py and
 test_decode_scored.py."""
+import contextlib
+import types
+
 import pytest
 import torch
 
-from paged_kv_cache_466_b200 import PA_DERR_BAD_SEQ, pa_decode_scored, pa_prefill
+import paged_kv_cache_466_b200 as pa
+from paged_kv_cache_466_b200 import (PA_DERR_BAD_SEQ, KVPool, Rope, _lib, pa_decode_scored,
+                                     pa_kv_append_rope, pa_prefill)
 from tests.helpers import DEV
 from tests.scored_ref import make_batch
 from tests.test_decode_scored import _check as _check_step
@@ -122,3 +127,101 @@ def test_a_step_whose_query_is_not_a_number_gives_nan(kind, G):
         assert torch.isnan(got[sick]).all() and torch.all(got[3] == 0)
         got[sick] = clean[sick]
         _check_step(pool, q, bt, ctx, 0.1, got, **kw)
+
+
+@gpu
+def test_calls_on_a_stream_allocate_for_that_stream():
+    """Only stream= is given, while the current stream is busy and then refills what it can get
+    of the freed storage: outputs and workspaces of the calls must not meet either."""
+    B, Hq, D = 3, 8, 128
+    lens, qlens = [3000, 900, 17], [9, 4, 1]
+    pool, bt, ctx, g = make_batch(lens, Hq, 2, D, 16, "bf16")
+    q, begin, n = _queries(g, qlens, Hq, D)
+    q = q[:n].contiguous()
+    step = torch.randn(B, Hq, D, generator=g, device=DEV).to(torch.bfloat16)
+    rope = Rope.from_base(4000, D, 10000.0, DEV)
+    k, v = (torch.randn(n, 2, D, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
+    spare = KVPool(8, 2, 16, D, "bf16", DEV, fill_byte=0)
+    seq = torch.zeros(n, dtype=torch.int32, device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None].contiguous()
+
+    def calls(stream):
+        return (pa_prefill(pool, q, begin, bt, ctx, 0.09, num_splits=4, stream=stream),
+                pa_decode_scored(pool, step, bt, ctx, 0.09, softcap=9.0, num_splits=4, stream=stream),
+                pa_kv_append_rope(spare, rope, q, k, v, seq, pos, table, stream=stream),
+                pa.pa_decode(pool, step, bt, ctx, 0.09, num_splits=4, stream=stream),
+                pa.pa_decode_range(pool, step, bt, ctx, 0.09, 0, 3008, num_splits=4, stream=stream)[0])
+
+    want = [t.clone() for t in calls(None)]
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        busy = busy @ busy * 1e-3                     # the current stream is behind
+        got = calls(side)
+        for size in (1 << 12, 1 << 16, 1 << 20, 1 << 22):
+            for _ in range(8):
+                torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+        torch.cuda.current_stream().wait_stream(side)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        del got, x
+
+
+def test_storage_of_a_call_is_allocated_on_its_stream(monkeypatch):
+    """Without a GPU: every tensor that a call with stream= makes is made with that stream as the
+    current one, and its outputs are recorded on the caller's."""
+    current, made, recorded = ["the current stream"], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def watched(make):
+        def f(*a, **kw):
+            made.append(current[-1])
+            return make(*a, **kw)
+        return f
+
+    class Library:                                    # every call succeeds; sizes are 4096
+        def __getattr__(self, name):
+            return lambda *a: (4096 if name.endswith("_bytes") else 2 if "splits" in name else 0)
+
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    pool = KVPool(2, 1, 16, 64, "bf16", "cpu")
+    rope = Rope(torch.zeros(4, 64))
+    z = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    one, bt = i32(1), i32(0).view(1, 1)
+    parts, lse = torch.zeros(2, 1, 1, 64), torch.zeros(2, 1, 1)
+    packet = types.SimpleNamespace(shape=(1, 1, 1, 1), dev=z, host=z, nbytes=1)
+    out_host = torch.zeros(1, 1, 64)
+    monkeypatch.setattr(_lib, "load", Library)
+    monkeypatch.setattr(_lib, "check", lambda *a: None)
+    monkeypatch.setattr(pa, "_need_device", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append(s))
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, watched(getattr(torch, name)))
+    monkeypatch.setattr(torch.Tensor, "new_empty", watched(torch.Tensor.new_empty))
+    side = types.SimpleNamespace(cuda_stream=5)
+    for call, outputs in (
+            (lambda: pa_prefill(pool, z, i32(0, 1), bt, one, 0.1, stream=side), 1),
+            (lambda: pa_decode_scored(pool, z, bt, one, 0.1, stream=side), 1),
+            (lambda: pa_kv_append_rope(pool, rope, z, z, z, one, one, bt, stream=side), 1),
+            (lambda: pa.pa_decode(pool, z, bt, one, 0.1, stream=side), 1),
+            (lambda: pa.pa_decode_append(pool, z, z, z, bt, one, 0.1, stream=side), 1),
+            (lambda: pa.pa_decode_shared_prefix(pool, z, one, 16, bt, one, 0.1, stream=side), 1),
+            (lambda: pa.pa_decode_window(pool, z, bt, one, 0.1, 1, 1, stream=side), 1),
+            (lambda: pa.pa_decode_range(pool, z, bt, one, 0.1, 0, 1, stream=side), 2),
+            (lambda: pa.pa_decode_step_host(pool, packet, 0.1, out_host, stream=side), 1),
+            (lambda: pa.pa_splitkv_reduce(parts[None, 0], lse[None, 0], stream=side), 1),
+            (lambda: pa.pa_merge_partials(parts, lse, stream=side), 2)):
+        made.clear()
+        recorded.clear()
+        call()
+        assert made and all(s is side for s in made)
+        assert recorded == ["the current stream"] * outputs
