@@ -1114,15 +1114,16 @@ cudaError_t launch_t(const PrefillArgs &a_in, cudaStream_t stream) {
   PrefillArgs a = a_in;
   // cap tanh(z), z = cap_z u, as u R(u^2), fitted for the least absolute error
   // of tanh, 1.9e-7, on |z| <= 1/2; u is q.k (bf16 pools) or the score in log2
-  // units. Coefficients that fp32 cannot hold (a tiny cap or scale) leave the
-  // bound at 0: such scores take the other way.
+  // units. Coefficients that fp32 cannot hold, or not to its full precision (a
+  // tiny cap or scale, a huge cap), leave the bound at 0: such scores take the
+  // other way.
   const double z = KVT == PA_KV_BF16 ? (double)a.scale_log2 * a.inv_cap : (double)a.inv_cap;
   const double c[4] = {1.0, -0.333264608, 0.131858621, -0.044229293};
   double zz = z;
   bool fits = a.cap_l2 > 0.f && z > 0.0 && 0.5 / z < 1e18;  // (the bound is used squared)
   for (int i = 0; i < 4; ++i, zz *= z * z) {
     a.cap_r[i] = (float)(a.cap_l2 * c[i] * zz);
-    fits = fits && std::isfinite(a.cap_r[i]);
+    fits = fits && std::isnormal(a.cap_r[i]);
   }
   a.cap_u = fits ? (float)(0.5 / z) : 0.f;
   if (a.slopes != nullptr)

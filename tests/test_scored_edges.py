@@ -130,6 +130,21 @@ def test_a_step_whose_query_is_not_a_number_gives_nan(kind, G):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8"])
+@pytest.mark.parametrize("scale,cap", [(1e-5, 50.0), (1e-8, 30.0), (1e-12, 30.0), (0.09, 1e6),
+                                       (1e-3, 50.0)])
+def test_caps_with_small_scales(kind, scale, cap):
+    """Scores of ordinary size made of large products and a small scale (and a large cap): the
+    short polynomial of the cap is left before one of its coefficients loses bits."""
+    qlens, lens = [300, 40], [900, 640]
+    amp = (0.1 * min(cap, 60.0) / (scale * 128 ** 0.5)) ** 0.5   # a tenth of the cap
+    pool, bt, ctx, g = make_batch(lens, 4, 2, 128, 16, kind, amp=amp)
+    q, begin, n = _queries(g, qlens, 4, 128, amp)
+    got, lse = _run(pool, q, begin, bt, ctx, scale, {"softcap": cap}, num_splits=1)
+    _check(pool, q, begin, bt, ctx, scale, n, got, lse, softcap=cap)
+
+
+@gpu
 def test_calls_on_a_stream_allocate_for_that_stream():
     """Only stream= is given, while the current stream is busy and then refills what it can get
     of the freed storage: outputs and workspaces of the calls must not meet either."""
