@@ -373,7 +373,7 @@ pa_status_t pa_decode_append(const pa_kv_pool_t *pool, const void *q,
  * of the context must be finite, also those that are masked.
  */
 typedef struct {
-  float softcap;               /* >= 0; 0: scores are not capped                 */
+  float softcap;               /* 2^-126 .. 2^125; 0: scores are not capped      */
   const float *alibi_slopes;   /* (device) fp32 [num_q_heads], or NULL           */
   const int32_t *doc_begin;    /* (device) int32, one per query token: the first
                                   position of its document (a sequence may hold

@@ -633,9 +633,11 @@ namespace {
 
 pa_status_t check_score(const pa_score_t *score) {
   if (score == nullptr) return PA_OK;
-  if (!(score->softcap >= 0.f) || score->softcap > 3.0e38f)
-    return fail(PA_ERR_INVALID_ARG, "softcap=%g (0 or a positive finite number)",
-                (double)score->softcap);
+  // the kernels hold softcap * log2(e) and its reciprocal: both stay normal
+  // numbers in this range
+  const float cap = score->softcap;
+  if (!(cap == 0.f || (cap >= 0x1p-126f && cap <= 0x1p125f)))
+    return fail(PA_ERR_INVALID_ARG, "softcap=%g (0, or from 2^-126 to 2^125)", (double)cap);
   return PA_OK;
 }
 

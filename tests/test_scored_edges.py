@@ -4,6 +4,7 @@ scales at the ends of their range, storage that a call allocates. The 64-bit
 definitions and the tolerances are those of test_prefill.py and
 test_decode_scored.py."""
 import contextlib
+import ctypes
 import types
 
 import pytest
@@ -12,6 +13,7 @@ import torch
 import paged_kv_cache_466_b200 as pa
 from paged_kv_cache_466_b200 import (PA_DERR_BAD_SEQ, KVPool, Rope, _lib, pa_decode_scored,
                                      pa_kv_append_rope, pa_prefill)
+from paged_kv_cache_466_b200._lib import PA_ERR_INVALID_ARG, PA_OK, pa_kv_pool_t, pa_score_t
 from tests.helpers import DEV
 from tests.scored_ref import make_batch
 from tests.test_decode_scored import _check as _check_step
@@ -142,6 +144,45 @@ def test_caps_with_small_scales(kind, scale, cap):
     q, begin, n = _queries(g, qlens, 4, 128, amp)
     got, lse = _run(pool, q, begin, bt, ctx, scale, {"softcap": cap}, num_splits=1)
     _check(pool, q, begin, bt, ctx, scale, n, got, lse, softcap=cap)
+
+
+@gpu
+@pytest.mark.parametrize("cap", [2.0 ** 125, 2.0 ** -126])
+def test_largest_and_smallest_cap(cap):
+    """The largest cap changes nothing, the smallest makes all scores equal; a query of zeros
+    has scores of exactly 0 (whose product with an infinite factor would be NaN)."""
+    lens = [500, 130]
+    pool, bt, ctx, g = make_batch(lens, 4, 2, 128, 16, "bf16")
+    q, begin, n = _queries(g, [40, 130], 4, 128)
+    q[39, 1] = 0
+    got, lse = _run(pool, q, begin, bt, ctx, 0.1, {"softcap": cap})
+    as_if = 0.0 if cap > 1 else cap
+    _check(pool, q, begin, bt, ctx, 0.1, n, got, lse, softcap=as_if)
+    last = q[[39, 169]].contiguous()
+    step = pa_decode_scored(pool, last, bt, ctx, 0.1, softcap=cap)
+    _check_step(pool, last, bt, ctx, 0.1, step, softcap=as_if)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_kv_cache_466_b200 import build
+    build.build()
+    return _lib.load()
+
+
+def test_caps_out_of_range_are_refused(lib):
+    """softcap * log2(e) and its reciprocal have to be normal fp32 numbers (no call launches)."""
+    pool = pa_kv_pool_t(num_pages=8, page_size=16, num_kv_heads=2, head_dim=128, dtype=0, k_pool=0x1000,
+                        v_pool=0x2000, k_sz=None, v_sz=None)
+    for cap, status in ((2.0 ** 125, PA_OK), (1.01 * 2.0 ** 125, PA_ERR_INVALID_ARG),
+                        (2.5e38, PA_ERR_INVALID_ARG), (2.0 ** -126, PA_OK),
+                        (0.99 * 2.0 ** -126, PA_ERR_INVALID_ARG), (1e-44, PA_ERR_INVALID_ARG),
+                        (0.0, PA_OK), (50.0, PA_OK)):
+        score = ctypes.byref(pa_score_t(cap, None, None, None))
+        assert lib.pa_prefill(ctypes.byref(pool), score, None, 0, 4, None, 0, None, 4, None, 0.1, None,
+                              None, None, 0, 1, None, None) == status
+        assert lib.pa_decode_scored(ctypes.byref(pool), score, None, None, None, None, None, 0, 4, None, 4,
+                                    None, 0.1, None, None, 0, 1, None, None) == status
 
 
 @gpu
