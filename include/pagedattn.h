@@ -433,9 +433,13 @@ pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
  *   lse_out  : (device) fp32 [num_tokens][num_q_heads], natural log of the sum
  *              of exp(x) over the visible keys (-inf: none), or NULL
  *   num_splits : 0 = automatic: the keys are split over CTAs when there are few
- *              query rows, and the partials merged by a second launch
- *   workspace : (device) >= pa_prefill_workspace_bytes(...) bytes, 256-byte
- *              aligned; NULL when that is 0. May be shared with other entry
+ *              query rows, and the partials merged by a second launch. Fewer
+ *              query rows are split more, so the workspace for a small batch can
+ *              be the larger one; automatic splits are lowered to what the given
+ *              workspace holds (down to one, which needs none)
+ *   workspace : (device) pa_prefill_workspace_bytes(...) bytes for the whole
+ *              split count, 256-byte aligned; with num_splits == 0 any size, or
+ *              NULL, will do. May be shared with other entry
  *              points (see pa_decode_workspace_bytes); the calls must not overlap
  * All cache formats. A page id outside the pool is flagged PA_DERR_BAD_PAGE and
  * its tokens are left out. The softmax weights are rounded to bf16 for the

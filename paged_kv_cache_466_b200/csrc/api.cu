@@ -756,9 +756,17 @@ pa_status_t pa_prefill(const pa_kv_pool_t *pool, const pa_score_t *score, const 
     return fail(PA_ERR_INVALID_ARG, "q, q_begin, block_tables, context_lens and out are required");
   if (!aligned(q, 16) || !aligned(out, 16))
     return fail(PA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  const int S = prefill_splits(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits);
-  const size_t parts = (size_t)num_tokens * num_q_heads * S * sizeof(float);
-  const size_t o_bytes = align256(parts * pool->head_dim);
+  int S = prefill_splits(pool, num_tokens, num_seqs, num_q_heads, max_pages, num_splits);
+  size_t parts, o_bytes;
+  // an automatic split count is lowered to what the workspace holds (it rises
+  // as the batch shrinks, so a workspace for the largest batch may be too small)
+  for (;; --S) {
+    parts = (size_t)num_tokens * num_q_heads * S * sizeof(float);
+    o_bytes = align256(parts * pool->head_dim);
+    if (S <= 1 || num_splits != 0 ||
+        (workspace != nullptr && workspace_fits(workspace_bytes, o_bytes + align256(parts), 0)))
+      break;
+  }
   if (S > 1) {
     if (workspace == nullptr || !workspace_fits(workspace_bytes, o_bytes + align256(parts), 0))
       return fail(PA_ERR_WORKSPACE, "workspace: need %zu bytes for %d splits, got %zu",

@@ -12,7 +12,7 @@ import torch
 
 import paged_kv_cache_466_b200 as pa
 from paged_kv_cache_466_b200 import (PA_DERR_BAD_SEQ, KVPool, Rope, _lib, pa_decode_scored,
-                                     pa_kv_append_rope, pa_prefill)
+                                     pa_kv_append_rope, pa_prefill, pa_prefill_workspace_bytes)
 from paged_kv_cache_466_b200._lib import PA_ERR_INVALID_ARG, PA_OK, pa_kv_pool_t, pa_score_t
 from tests.helpers import DEV
 from tests.scored_ref import make_batch
@@ -183,6 +183,26 @@ def test_caps_out_of_range_are_refused(lib):
                               None, None, 0, 1, None, None) == status
         assert lib.pa_decode_scored(ctypes.byref(pool), score, None, None, None, None, None, 0, 4, None, 4,
                                     None, 0.1, None, None, 0, 1, None, None) == status
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bf16", "u8"])
+def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(kind):
+    """The automatic split count rises as the batch shrinks: what the workspace cannot hold is
+    not split, and nothing behind the given size is written."""
+    pool, bt, ctx, g = make_batch([3000], 8, 2, 128, 16, kind)
+    size = lambda n, s=0: pa_prefill_workspace_bytes(pool, n, 1, 8, bt.shape[1], s)
+    q, begin, n = _queries(g, [4], 8, 128)
+    N = q.shape[0]
+    whole = size(N)
+    assert size(3000) < whole                  # else there is nothing to lower here
+    for given in (size(3000), 256, size(N, 2), size(N, 3) - 256, size(N, 5), whole):
+        ws = torch.full((given + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        got, lse = _run(pool, q, begin, bt, ctx, 0.1, {}, workspace=ws[:given])
+        _check(pool, q, begin, bt, ctx, 0.1, n, got, lse)
+        assert torch.all(ws[given:] == 0x5A)
+    with pytest.raises(pa.PagedAttnError):     # an explicit count is not lowered
+        _run(pool, q, begin, bt, ctx, 0.1, {}, workspace=ws[:size(N, 2)], num_splits=3)
 
 
 @gpu
