@@ -128,6 +128,16 @@ def _need(t: torch.Tensor, name: str, dtype, device=None):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _workspace_bytes(workspace: Optional[torch.Tensor], device) -> int:
+    if workspace is None:
+        return 0
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _need_device(device, where: str, d_err: Optional[torch.Tensor]):
     """The call runs on the current device: the pool must be there, and the error word."""
     if device.type != "cuda" or device.index != _current_device():
@@ -356,7 +366,7 @@ def pa_decode(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
         need = pa_decode_workspace_bytes(B, Hq, D, S)
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode(ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables),
                                max_pages, _ptr(context_lens), float(scale), _ptr(out),
                                _ptr(workspace), ws_bytes, num_splits, _ptr(d_err),
@@ -397,7 +407,7 @@ def pa_decode_append(pool: KVPool, q: torch.Tensor, k_new: torch.Tensor, v_new: 
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     if host_context_lens is not None:
         hl = host_context_lens
         if not (isinstance(hl, np.ndarray) and hl.dtype == np.int32 and hl.flags.c_contiguous):
@@ -484,7 +494,7 @@ def pa_decode_scored(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode_scored(
         ctypes.byref(pool.c), ctypes.byref(score), None if rope is None else ctypes.byref(rope.c),
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(rope_pos), B, Hq, _ptr(block_tables), max_pages,
@@ -541,7 +551,7 @@ def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_table
         need = pa_prefill_workspace_bytes(pool, N, B, Hq, max_pages, num_splits)
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream)  # (partials: written before they are read)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_prefill(
         ctypes.byref(pool.c), ctypes.byref(score), _ptr(q), N, Hq, _ptr(q_begin), B,
         _ptr(block_tables), max_pages, _ptr(context_lens), float(scale), _ptr(out), _ptr(lse_out),
@@ -581,7 +591,7 @@ def pa_decode_shared_prefix(pool: KVPool, q: torch.Tensor, prefix_pages: torch.T
         need = pa_decode_shared_prefix_workspace_bytes(pool, B, Hq, max_pages, prefix_len,
                                                        num_splits)
         workspace = _own(max(need, 256), torch.uint8, dev, stream, zero=True)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode_shared_prefix(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(prefix_pages), int(prefix_len),
         _ptr(block_tables), max_pages, _ptr(context_lens), float(scale), _ptr(out),
@@ -622,7 +632,7 @@ def pa_decode_window(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
                                           pa_decode_num_splits(pool, B, max_pages, num_splits)))
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode_window(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables), max_pages, _ptr(context_lens),
         int(sinks), int(window), float(scale), _ptr(out), _ptr(workspace), ws_bytes,
@@ -702,7 +712,7 @@ def pa_decode_step_host(pool: KVPool, packet: StepPacket, scale: float, out_host
                                          pa_decode_num_splits(pool, B, max_pages, num_splits))
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode_step_host(
         ctypes.byref(pool.c), ctypes.c_void_p(packet.host.data_ptr()), _ptr(packet.dev),
         packet.nbytes, B, Hq, max_pages, num_new, float(scale), _ptr(out_dev),
@@ -741,7 +751,7 @@ class StepGraph:
             if need > 0:
                 workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
                 torch.cuda.current_stream(dev).synchronize()  # a launch may go to any stream
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = _workspace_bytes(workspace, dev)
         # keep every buffer the graph points at alive as long as the graph
         self._keep = (pool, packet, out_host, out_dev, workspace, d_err)
         self.out_host = out_host
@@ -851,7 +861,7 @@ def pa_decode_range(pool: KVPool, q: torch.Tensor, block_tables: torch.Tensor,
                                                num_splits)
         if need > 0:
             workspace = _own(need, torch.uint8, dev, stream, zero=True)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     st = _lib.load().pa_decode_range(
         ctypes.byref(pool.c), _ptr(q), B, Hq, _ptr(block_tables), max_pages, _ptr(context_lens),
         int(tok_begin), int(tok_end), float(scale), _ptr(o_out), _ptr(lse_out), _ptr(workspace),

@@ -245,6 +245,37 @@ def test_calls_on_a_stream_allocate_for_that_stream():
         del got, x
 
 
+class Library:
+    """A library whose every call succeeds: sizes are 4096, split counts 2."""
+
+    def __getattr__(self, name):
+        return lambda *a: (4096 if name.endswith("_bytes") else 2 if "splits" in name else 0)
+
+
+def test_workspaces_elsewhere_are_refused(monkeypatch):
+    """A workspace on another device than the pool, or with gaps, never reaches a kernel."""
+    monkeypatch.setattr(_lib, "load", Library)
+    monkeypatch.setattr(pa, "_need_device", lambda *a: None)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    pool = KVPool(2, 1, 16, 64, "bf16", "cpu")
+    z = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    one, bt = i32(1), i32(0).view(1, 1)
+    for ws in (torch.empty(4096, dtype=torch.uint8, device="meta"),
+               torch.empty(8192, dtype=torch.uint8)[::2]):
+        kw = dict(workspace=ws, stream=types.SimpleNamespace(cuda_stream=0))
+        out = torch.zeros(1, 1, 64)
+        for call in (lambda: pa_prefill(pool, z, i32(0, 1), bt, one, 0.1, out=z.clone(), **kw),
+                     lambda: pa_decode_scored(pool, z, bt, one, 0.1, out=out, **kw),
+                     lambda: pa.pa_decode(pool, z, bt, one, 0.1, out=out, **kw),
+                     lambda: pa.pa_decode_append(pool, z, z, z, bt, one, 0.1, out=out, **kw),
+                     lambda: pa.pa_decode_shared_prefix(pool, z, one, 16, bt, one, 0.1, out=out, **kw),
+                     lambda: pa.pa_decode_window(pool, z, bt, one, 0.1, 1, 1, out=out, **kw),
+                     lambda: pa.pa_decode_range(pool, z, bt, one, 0.1, 0, 1, o_out=out,
+                                                lse_out=torch.zeros(1, 1), **kw)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+
+
 def test_storage_of_a_call_is_allocated_on_its_stream(monkeypatch):
     """Without a GPU: every tensor that a call with stream= makes is made with that stream as the
     current one, and its outputs are recorded on the caller's."""
@@ -261,10 +292,6 @@ def test_storage_of_a_call_is_allocated_on_its_stream(monkeypatch):
             made.append(current[-1])
             return make(*a, **kw)
         return f
-
-    class Library:                                    # every call succeeds; sizes are 4096
-        def __getattr__(self, name):
-            return lambda *a: (4096 if name.endswith("_bytes") else 2 if "splits" in name else 0)
 
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
     pool = KVPool(2, 1, 16, 64, "bf16", "cpu")
