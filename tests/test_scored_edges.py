@@ -15,7 +15,7 @@ from paged_kv_cache_466_b200 import (PA_DERR_BAD_SEQ, KVPool, Rope, _lib, pa_dec
                                      pa_kv_append_rope, pa_prefill, pa_prefill_workspace_bytes)
 from paged_kv_cache_466_b200._lib import PA_ERR_INVALID_ARG, PA_OK, pa_kv_pool_t, pa_score_t
 from tests.helpers import DEV
-from tests.scored_ref import make_batch
+from tests.scored_ref import attend64, make_batch
 from tests.test_decode_scored import _check as _check_step
 from tests.test_prefill import _check, _queries, _run
 
@@ -129,6 +129,30 @@ def test_a_step_whose_query_is_not_a_number_gives_nan(kind, G):
         assert torch.isnan(got[sick]).all() and torch.all(got[3] == 0)
         got[sick] = clean[sick]
         _check_step(pool, q, bt, ctx, 0.1, got, **kw)
+
+
+@gpu
+@pytest.mark.parametrize("kind,most", [("bf16", 1.5e-6), ("fp8", 1.5e-6), ("u8", 1.5e-6), ("u4", 5e-6)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_contexts_keep_the_bits_of_their_weights(kind, most, D):
+    """The scored step's error in the 2-norm at 30,000 keys in one split. Independent errors:
+    a weight carries its score's (the sum of q.k, about 2e-7 rms) and the exponential's (2^-22 at
+    most, 1.5e-7 rms); a block's 16 products are summed with 1.2e-7; the 235 sums of a warp's
+    blocks, which grow as their square root, are added with roundings of 2^-24, together
+    2^-24 sqrt(235 / 2) / sqrt(3) = 3.7e-7. In all 4.6e-7, a third of the bound. Weights cut to
+    two bf16 operands alone are 2.4e-6 off, sums cut off toward zero in place 9e-6.
+    INT4: a row's centre z + 8 s lies half a step (0.16 of the deviation) beside 0, so the sum of
+    p z grows to 0.16 sqrt(30000) = 28 times the output; a lane's 120 additions of it round with
+    2^-24 sqrt(120 / 3) of it at most, 1e-5 for one lane, which 64 lanes' independent signs make
+    1.3e-6; the same again for the terms that it meets in O."""
+    pool, bt, ctx, g = make_batch([30000, 12345], 8, 1, D, 32, kind, seed=2)
+    q = torch.randn(2, 8, D, generator=g, device=DEV).to(torch.bfloat16)
+    for cap in (0.0, 30.0):
+        got = pa_decode_scored(pool, q, bt, ctx, D ** -0.5, softcap=cap, num_splits=1)
+        want, _, _ = attend64(pool, q, [0, 1, 2], bt, ctx.tolist(), D ** -0.5, cap)
+        rel = float((got.double() - want).norm() / want.norm())
+        print(f"rel {rel:.2e}")
+        assert rel <= most
 
 
 @gpu
