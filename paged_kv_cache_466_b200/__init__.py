@@ -524,7 +524,8 @@ def pa_prefill(pool: KVPool, q: torch.Tensor, q_begin: torch.Tensor, block_table
     tokens; causal unless ``prefix_end`` [N] (positions below it are seen by that
     token in any case) says otherwise, from ``doc_begin`` [N] on. Scores are
     capped with ``softcap`` > 0 and biased by -``alibi_slopes``[head] x distance.
-    ``lse_out`` fp32 [N, Hq] also receives the log-sum-exps."""
+    ``lse_out`` fp32 [N, Hq] also receives the log-sum-exps. Rows behind the last
+    sequence are not written: an ``out`` that the call allocates holds anything there."""
     dev = pool.device
     _need_device(dev, "pa_prefill", d_err)
     _need(q, "q", torch.bfloat16, dev)

@@ -210,9 +210,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // tanh to fp32 accuracy (the hardware's tanh is good to 2^-11 only, which a cap
 // of 50 would turn into 2 % of a softmax weight). Up to |z| = 5/8 an odd
-// polynomial, z + z^3 Q(z^2), Q fitted by weighted least squares for the least
-// relative error (4.4e-9); beyond it 1 - 2 / (e^{2z} + 1), whose absolute error
-// of about 1e-7 no longer cancels.
+// polynomial, z + z^3 Q(z^2), Q fitted for the least largest relative error
+// (4.4e-9: Lawson's method, least squares whose weights grow where the error is
+// largest until it is level); beyond it 1 - 2 / (e^{2z} + 1), whose absolute
+// error of about 1e-7 no longer cancels.
 __device__ __forceinline__ float tanh_f32(float z) {
   const float z2 = z * z;
   float q = fmaf(-0.00570498f, z2, 0.02063908f);
