@@ -1020,17 +1020,18 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a)
   if (row >= (size_t)a.n * a.hq) return;  // (the grid is rounded up to whole CTAs)
   // Rows outside the sequences, clamped as prefill_kernel clamps them, have no
   // partials and are left as they were.
-  const int tok = (int)(row / a.hq);
+  const float *lse = a.lse_part + row * a.S;
+  float M = lane < a.S ? __ldcg(lse + lane) : -INFINITY;  // on its way meanwhile
+  const int tok = (int)((uint32_t)row / (uint32_t)a.hq);  // (at most 2^31 rows)
   bool mine = false;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B && !mine; b0 += 32) {
-    const int b = b0 + lane;
-    mine = __any_sync(0xffffffffu, b < a.B && tok >= max(__ldg(a.q_begin + min(b, a.B)), 0) &&
-                                       tok < min(__ldg(a.q_begin + min(b + 1, a.B)), a.n));
+    const int b = min(b0 + lane, a.B - 1);
+    const int q0 = __ldg(a.q_begin + b), q1 = __ldg(a.q_begin + b + 1);
+    mine = __any_sync(0xffffffffu, tok >= max(q0, 0) && tok < min(q1, a.n));
   }
   if (!mine) return;
-  const float *lse = a.lse_part + row * a.S;
-  float M = -INFINITY;
-  for (int s = lane; s < a.S; s += 32) M = fmaxf(M, __ldcg(lse + s));
+  for (int s = lane + 32; s < a.S; s += 32) M = fmaxf(M, __ldcg(lse + s));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int E = D / 32;
