@@ -442,8 +442,9 @@ pa_status_t pa_decode_scored(const pa_kv_pool_t *pool, const pa_score_t *score,
  *              NULL, will do. May be shared with other entry
  *              points (see pa_decode_workspace_bytes); the calls must not overlap
  * All cache formats. A page id outside the pool is flagged PA_DERR_BAD_PAGE and
- * its tokens are left out. The softmax weights are rounded to bf16 for the
- * second product, sums and statistics are fp32. Deterministic.
+ * its tokens are left out. The softmax weights (quantised pools: the weight
+ * times its value row's scale) are rounded to bf16 for the second product, sums
+ * and statistics are fp32. Deterministic.
  */
 size_t pa_prefill_workspace_bytes(const pa_kv_pool_t *pool, int32_t num_tokens,
                                   int32_t num_seqs, int32_t num_q_heads,
