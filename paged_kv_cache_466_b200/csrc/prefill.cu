@@ -127,6 +127,7 @@ struct Control {
   uint64_t q_full;               // queries in shared memory
   uint64_t s_full[2];            // scores of a row tile (and the PV before them) done
   uint64_t p_full[2];            // P of a row tile stored, O rescaled
+  uint64_t stopped;              // MMAs in flight when the block gives up are done
   uint32_t tmem;
   int32_t dead;                  // a bounded wait ran out: everybody stops
   int32_t seq, blk, q0, qlen, ctx;
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
       bar_init(smem_u32(&c.p_full[i]), kTile);
     }
     bar_init(smem_u32(&c.q_full), kSoftmaxThreads);
+    bar_init(smem_u32(&c.stopped), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -602,6 +604,12 @@ __global__ void __launch_bounds__(kThreads<KVT>, 1)
             if (k + 1 < n) umma_commit(smem_u32(&c.empty[(2 * k + 2) % L::kSlots]));
           }
           __syncwarp();
+        }
+        if (!ok) {
+          // stopped early: the MMAs in flight must end before their tensor memory is freed
+          if (elect_one()) umma_commit(smem_u32(&c.stopped));
+          __syncwarp();
+          mbar_wait_bounded(smem_u32(&c.stopped), 0, kWaitLimitNs);
         }
       }
     } else if constexpr (!kQuant) {
